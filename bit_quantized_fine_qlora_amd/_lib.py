@@ -71,6 +71,22 @@ PROTOTYPES = {
     "qlora_linear_bwd_ex": (ctypes.c_int, [c_i64, c_i64, c_i64, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
                                            c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.POINTER(Dropout), c_vp, c_sz,
                                            c_vp]),
+    "qlora_checkpoint_pack": (ctypes.c_int, [c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "qlora_checkpoint_unpack": (ctypes.c_int, [c_i64, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "qlora_linear_bwd_ckpt": (ctypes.c_int, [c_i64, c_i64, c_i64, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                             c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, ctypes.POINTER(Dropout), c_vp,
+                                             c_sz, c_vp]),
+    "qlora_norm_fwd": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i64, c_i64, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_vp]),
+    "qlora_norm_workspace_bytes": (c_sz, [c_i32, c_i64, c_i64, c_i32]),
+    "qlora_norm_bwd": (ctypes.c_int, [c_i32, c_i32, c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                      c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "qlora_preference_workspace_bytes": (c_sz, [c_i64, c_i64, c_i64]),
+    "qlora_sequence_logps": (ctypes.c_int, [c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz,
+                                            c_vp]),
+    "qlora_preference_fwd": (ctypes.c_int, [c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_f32, c_f32, c_vp,
+                                            c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "qlora_preference_bwd": (ctypes.c_int, [c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_f32, c_vp, c_vp]),
     "qlora_linear_check": (ctypes.c_int, [ctypes.c_int, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp]),
     "qlora_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "qlora_profile_query": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(c_i64), ctypes.POINTER(ctypes.c_double)]),

@@ -32,6 +32,34 @@ class QuantizedWeight:
         return self.codes.numel() + self.absmax8.numel() + 4 * self.c2.numel()
 
 
+@dataclasses.dataclass
+class Checkpoint8:
+    """A bf16 [M, n] tensor kept in 8 bits: codes and one scale byte per 32 values of a row."""
+    codes: torch.Tensor     # int8 [M, n]
+    scales: torch.Tensor    # uint8 [M, 4 ceil(n / 128)]
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.scales.numel()
+
+    def check(self, name: str) -> None:
+        M, n = self.codes.shape
+        _need(self.codes, torch.int8, (M, n), name + ".codes")
+        _need(self.scales, torch.uint8, (M, checkpoint_pitch(n)), name + ".scales")
+
+
+def checkpoint_pitch(n: int) -> int:
+    """Bytes in a row of a Checkpoint8's scales."""
+    return (n + 127) // 128 * 4
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -327,12 +355,21 @@ def linear_bwd(x: torch.Tensor, g: torch.Tensor, q: QuantizedWeight, A: torch.Te
     """Returns (grad_x bf16 [M, n] or None, grad_A bf16 [r, n], grad_B bf16 [m, r]).
 
     dropout: the forward's (p, seed, offset), or None; u, when given, is the
-    forward's u (with the mask).
+    forward's u (with the mask).  x may be the saved input's Checkpoint8; u is
+    then required.
     """
+    ckpt = isinstance(x, Checkpoint8)
     M, n = x.shape
     m = q.m
     r = A.shape[0]
-    _need(x, torch.bfloat16, (M, q.n), "x")
+    if ckpt:
+        if u is None:
+            raise ValueError("u: required with a checkpointed input")
+        if n != q.n:
+            raise ValueError(f"x: expected a checkpoint of {(M, q.n)}, got one of {(M, n)}")
+        x.check("x")
+    else:
+        _need(x, torch.bfloat16, (M, q.n), "x")
     _need(g, torch.bfloat16, (M, m), "g")
     _need(A, torch.bfloat16, (r, n), "A")
     _need(B, torch.bfloat16, (m, r), "B")
@@ -344,7 +381,15 @@ def linear_bwd(x: torch.Tensor, g: torch.Tensor, q: QuantizedWeight, A: torch.Te
         gB = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
     else:
         gx, gA, gB = out
-    if dropout is None:
+    if ckpt:
+        op = QLORA_OP_BWD if dropout is None else QLORA_OP_BWD_DROPOUT
+        ws = _workspace(op, M, n, m, r, x.device, workspace)
+        st = _lib.load().qlora_linear_bwd_ckpt(M, n, m, r, float(s), _ptr(x.codes), _ptr(x.scales), _ptr(g),
+                                               _ptr(q.codes), _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(u),
+                                               _ptr(gx), _ptr(gA), _ptr(gB), _dropout(dropout), _ptr(ws), ws.numel(),
+                                               _stream(x.device))
+        _lib.check(st, "qlora_linear_bwd_ckpt")
+    elif dropout is None:
         ws = _workspace(QLORA_OP_BWD, M, n, m, r, x.device, workspace)
         st = _lib.load().qlora_linear_bwd(M, n, m, r, float(s), _ptr(x), _ptr(g), _ptr(q.codes), _ptr(q.absmax8),
                                           _ptr(q.c2), _ptr(A), _ptr(B), _ptr(u), _ptr(gx), _ptr(gA), _ptr(gB),
@@ -367,6 +412,210 @@ def linear_check(op: int, M: int, n: int, m: int, r: int, workspace: torch.Tenso
     dev = workspace.device if workspace is not None else None
     st = _lib.load().qlora_linear_check(int(op), M, n, m, r, _ptr(workspace), _stream(dev))
     _lib.check(st, "qlora_linear_check")
+
+
+def alloc_checkpoint(M: int, n: int, device="cuda") -> Checkpoint8:
+    return Checkpoint8(torch.empty((M, n), dtype=torch.int8, device=device),
+                       torch.empty((M, checkpoint_pitch(n)), dtype=torch.uint8, device=device))
+
+
+def checkpoint_pack(x: torch.Tensor, out: Checkpoint8 | None = None) -> Checkpoint8:
+    """The 8-bit checkpoint of a bf16 [M, n] tensor (qlora_checkpoint_pack)."""
+    M, n = x.shape
+    _need(x, torch.bfloat16, (M, n), "x")
+    if out is None:
+        out = alloc_checkpoint(M, n, x.device)
+    else:
+        _need(out.codes, torch.int8, (M, n), "out.codes")
+        out.check("out")
+    st = _lib.load().qlora_checkpoint_pack(M, n, _ptr(x), _ptr(out.codes), _ptr(out.scales), _stream(x.device))
+    _lib.check(st, "qlora_checkpoint_pack")
+    return out
+
+
+def checkpoint_unpack(c: Checkpoint8, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The bf16 [M, n] tensor that a checkpoint stands for."""
+    M, n = c.shape
+    c.check("c")
+    if out is None:
+        out = torch.empty((M, n), dtype=torch.bfloat16, device=c.device)
+    else:
+        _need(out, torch.bfloat16, (M, n), "out")
+    st = _lib.load().qlora_checkpoint_unpack(M, n, _ptr(c.codes), _ptr(c.scales), _ptr(out), _stream(c.device))
+    _lib.check(st, "qlora_checkpoint_unpack")
+    return out
+
+
+NORM_LAYER = 0
+NORM_RMS = 1
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_CKPT8 = 2
+
+
+def _type_of(t: torch.Tensor, name: str) -> int:
+    ty = _TYPES.get(t.dtype)
+    if ty is None:
+        raise TypeError(f"{name}: expected torch.bfloat16 or torch.float32, got {t.dtype}")
+    return ty
+
+
+def norm_fwd(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None, kind: int = NORM_RMS,
+             eps: float = 1e-5, checkpoint: bool = False, out: torch.Tensor | None = None):
+    """Layer norm (NORM_LAYER) or RMS norm (NORM_RMS) of the rows of x, bf16 or fp32 [M, n].
+
+    w, b: bf16 or fp32 [n] (fp32 with an fp32 x).  Returns (y, mean, rstd): y like x, mean (None for
+    NORM_RMS) and rstd fp32 [M]; with checkpoint=True (bf16 only) also the
+    Checkpoint8 of y.
+    """
+    M, n = x.shape
+    xt, wt = _type_of(x, "x"), _type_of(w, "w")
+    _need(x, x.dtype, (M, n), "x")
+    _need(w, w.dtype, (n,), "w")
+    if b is not None:
+        _need(b, w.dtype, (n,), "b")
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, x.dtype, (M, n), "out")
+    mean = torch.empty(M, dtype=torch.float32, device=x.device) if kind == NORM_LAYER else None
+    rstd = torch.empty(M, dtype=torch.float32, device=x.device)
+    y8 = alloc_checkpoint(M, n, x.device) if checkpoint else None
+    st = _lib.load().qlora_norm_fwd(int(kind), xt, wt, M, n, float(eps), _ptr(x), _ptr(w), _ptr(b), _ptr(out),
+                                    _ptr(mean), _ptr(rstd), _ptr(y8.codes) if y8 else None,
+                                    _ptr(y8.scales) if y8 else None, _stream(x.device))
+    _lib.check(st, "qlora_norm_fwd")
+    return (out, mean, rstd, y8) if checkpoint else (out, mean, rstd)
+
+
+def norm_bwd(x, g: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, mean: torch.Tensor | None = None,
+             bias: bool = False, need_grad_w: bool = True, out: torch.Tensor | None = None,
+             workspace: torch.Tensor | None = None):
+    """Backward of norm_fwd: (grad_x like g, grad_w, grad_b like w).
+
+    x: the forward's input or its Checkpoint8 (g is bf16 then).  mean: the
+    forward's, None for NORM_RMS.  grad_b is None without bias, both weights'
+    gradients without need_grad_w.
+    """
+    M, n = x.shape
+    if isinstance(x, Checkpoint8):
+        x.check("x")
+        xt, xp, xs, gtype = _CKPT8, _ptr(x.codes), _ptr(x.scales), torch.bfloat16
+    else:
+        xt, xp, xs, gtype = _type_of(x, "x"), _ptr(x), None, x.dtype
+        _need(x, x.dtype, (M, n), "x")
+    wt = _type_of(w, "w")
+    _need(g, gtype, (M, n), "g")
+    _need(w, w.dtype, (n,), "w")
+    _need(rstd, torch.float32, (M,), "rstd")
+    if mean is not None:
+        _need(mean, torch.float32, (M,), "mean")
+    if out is None:
+        out = torch.empty_like(g)
+    else:
+        _need(out, gtype, (M, n), "out")
+    gw = torch.empty_like(w) if need_grad_w else None
+    gb = torch.empty_like(w) if need_grad_w and bias else None
+    lib = _lib.load()
+    kind = NORM_RMS if mean is None else NORM_LAYER
+    need = int(lib.qlora_norm_workspace_bytes(kind, M, n, 2 if gb is not None else 1 if gw is not None else 0))
+    if need and (workspace is None or workspace.numel() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=g.device)
+    st = lib.qlora_norm_bwd(kind, xt, wt, M, n, xp, xs, _ptr(g), _ptr(w),
+                            _ptr(mean), _ptr(rstd), _ptr(out), _ptr(gw), _ptr(gb), _ptr(workspace),
+                            workspace.numel() if workspace is not None else 0, _stream(g.device))
+    _lib.check(st, "qlora_norm_bwd")
+    return out, gw, gb
+
+
+@dataclasses.dataclass
+class PreferenceResult:
+    """What preference_fwd returns; preference_bwd reads lse and coef."""
+    loss: torch.Tensor      # float32 [], mean over pairs
+    logps: torch.Tensor     # float32 [2 pairs]
+    lse: torch.Tensor       # float32 [T]
+    coef: torch.Tensor      # float32 [T], dloss / dlog-probability of each token
+
+
+def _packed(logits, labels, offsets):
+    T, V = logits.shape
+    ty = _type_of(logits, "logits")
+    _need(logits, logits.dtype, (T, V), "logits")
+    _need(labels, torch.int64, (T,), "labels")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"offsets: expected sequences + 1 values, got shape {tuple(offsets.shape)}")
+    _need(offsets, torch.int32, tuple(offsets.shape), "offsets")
+    return ty, T, V, offsets.numel() - 1
+
+
+def _preference_workspace(T, V, pairs, device, workspace):
+    need = int(_lib.load().qlora_preference_workspace_bytes(T, V, pairs))
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def sequence_logps(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor,
+                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Log-probability of each packed sequence (fp32 [sequences]).
+
+    logits: bf16 or fp32 [T, V], row t predicting labels[t] (int64 [T]; a
+    negative label takes its token out); sequence s is the tokens offsets[s]
+    .. offsets[s + 1] - 1 (int32 [sequences + 1], on the device).
+    """
+    ty, T, V, S = _packed(logits, labels, offsets)
+    dev = logits.device
+    logps = torch.empty(S, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    ws = _preference_workspace(T, V, 0, dev, workspace)
+    st = _lib.load().qlora_sequence_logps(ty, T, V, S, _ptr(logits), _ptr(labels), _ptr(offsets), _ptr(logps),
+                                          _ptr(lse), _ptr(ws), ws.numel(), _stream(dev))
+    _lib.check(st, "qlora_sequence_logps")
+    return logps
+
+
+def preference_fwd(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor,
+                   ref_logps: torch.Tensor | None = None, beta: float = 0.1, label_smoothing: float = 0.0,
+                   workspace: torch.Tensor | None = None) -> PreferenceResult:
+    """Preference loss of packed pairs: sequence 2i is preferred to sequence 2i + 1.
+
+    logits, labels, offsets as for sequence_logps; ref_logps: fp32 [2 pairs],
+    the reference model's log-probabilities (None: zeros).
+    """
+    ty, T, V, S = _packed(logits, labels, offsets)
+    if S % 2:
+        raise ValueError(f"offsets: pairs need an even number of sequences, got {S}")
+    if ref_logps is not None:
+        _need(ref_logps, torch.float32, (S,), "ref_logps")
+    dev = logits.device
+    loss = torch.empty((), dtype=torch.float32, device=dev)
+    logps = torch.empty(S, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    coef = torch.empty(T, dtype=torch.float32, device=dev)
+    ws = _preference_workspace(T, V, S // 2, dev, workspace)
+    st = _lib.load().qlora_preference_fwd(ty, T, V, S // 2, _ptr(logits), _ptr(labels), _ptr(offsets),
+                                          _ptr(ref_logps), float(beta), float(label_smoothing), _ptr(loss),
+                                          _ptr(logps), _ptr(lse), _ptr(coef), _ptr(ws), ws.numel(), _stream(dev))
+    _lib.check(st, "qlora_preference_fwd")
+    return PreferenceResult(loss, logps, lse, coef)
+
+
+def preference_bwd(logits: torch.Tensor, labels: torch.Tensor, saved: PreferenceResult, grad_scale: float = 1.0,
+                   out: torch.Tensor | None = None) -> torch.Tensor:
+    """grad_scale times the loss's gradient with respect to the logits (out may be the logits themselves)."""
+    T, V = logits.shape
+    ty = _type_of(logits, "logits")
+    _need(logits, logits.dtype, (T, V), "logits")
+    _need(labels, torch.int64, (T,), "labels")
+    _need(saved.lse, torch.float32, (T,), "saved.lse")
+    _need(saved.coef, torch.float32, (T,), "saved.coef")
+    if out is None:
+        out = torch.empty_like(logits)
+    else:
+        _need(out, logits.dtype, (T, V), "out")
+    st = _lib.load().qlora_preference_bwd(ty, T, V, _ptr(logits), _ptr(labels), _ptr(saved.lse), _ptr(saved.coef),
+                                          float(grad_scale), _ptr(out), _stream(logits.device))
+    _lib.check(st, "qlora_preference_bwd")
+    return out
 
 
 def profile_enable(on: bool = True) -> None:

@@ -65,6 +65,8 @@ void launch_down_proj(const uint16_t* X, int64_t M, int64_t K, const uint16_t* Y
 int token_grad_splits(int64_t M, int64_t J, int R);
 void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, int R, int splits, float* part,
                        hipStream_t stream, const DropoutDev* drop, uint16_t* planes, bool planes_ready);
+void launch_token_grad_ckpt(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t J, const float* Y, int R,
+                            int splits, float* part, hipStream_t stream, const DropoutDev& drop);
 size_t token_planes_bytes(int64_t M, int R);
 void launch_factor_planes(const float* Y, int nsplit, int64_t M, int R, uint16_t* P, float* Yout, const float* Y2,
                           uint16_t* P2, hipStream_t stream);
@@ -94,6 +96,24 @@ struct AdamTensorHost {
 };
 void launch_adam_step(const AdamTensorHost* ts, int count, float lr, float beta1, float beta2, float eps,
                       float weight_decay, int64_t step, hipStream_t stream);
+void launch_checkpoint_pack(int64_t M, int64_t n, const uint16_t* x, int8_t* codes, uint8_t* scales,
+                            hipStream_t stream);
+void launch_checkpoint_unpack(int64_t M, int64_t n, const int8_t* codes, const uint8_t* scales, uint16_t* x,
+                              hipStream_t stream);
+int64_t norm_max_width();
+size_t norm_bwd_ws_bytes(int layer, int64_t M, int64_t n, int accs);
+void launch_norm_fwd(int layer, int x_type, int w_f32, int64_t M, int64_t n, float eps, const void* x, const void* w,
+                     const void* b, void* y, float* mean, float* rstd, int8_t* codes, uint8_t* scales,
+                     hipStream_t stream);
+void launch_norm_bwd(int layer, int x_type, int w_f32, int64_t M, int64_t n, const void* x, const uint8_t* x_scales,
+                     const void* g, const void* w, const float* mean, const float* rstd, void* gx, int accs, void* gw,
+                     void* gb, float* part, hipStream_t stream);
+size_t pref_ws_bytes(int64_t T, int64_t V, int64_t pairs);
+void launch_pref_fwd(int type, int64_t T, int64_t V, int64_t seqs, int64_t pairs, const void* logits,
+                     const int64_t* labels, const int32_t* offsets, const float* ref, float beta, float smoothing,
+                     float* loss, float* logps, float* lse, float* coef, void* workspace, hipStream_t stream);
+void launch_pref_grad(int type, int64_t T, int64_t V, const void* logits, const int64_t* labels, const float* lse,
+                      const float* coef, float scale, void* grad, hipStream_t stream);
 bool gpass_supported(int R);
 int gpass_splits_f(int64_t M, int64_t J, int R);
 int gpass_splits_t(int64_t M);
@@ -723,21 +743,14 @@ qlora_status qlora_linear_fwd_grouped(int64_t M, int32_t count, const qlora_line
   return hip_status();
 }
 
-qlora_status qlora_linear_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
-                              const qlora_bf16* g, const uint8_t* codes, const uint8_t* absmax8, const float* c2,
-                              const qlora_bf16* A, const qlora_bf16* B, const float* u, qlora_bf16* grad_x,
-                              qlora_bf16* grad_A, qlora_bf16* grad_B, void* workspace, size_t workspace_bytes,
-                              qlora_stream_t stream) {
-  return qlora_linear_bwd_ex(M, n, m, r, s, x, g, codes, absmax8, c2, A, B, u, grad_x, grad_A, grad_B, nullptr,
-                             workspace, workspace_bytes, stream);
-}
-
-qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
-                                 const qlora_bf16* g, const uint8_t* codes, const uint8_t* absmax8,
-                                 const float* c2, const qlora_bf16* A, const qlora_bf16* B, const float* u,
-                                 qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
-                                 const qlora_dropout* dropout, void* workspace, size_t workspace_bytes,
-                                 qlora_stream_t stream) {
+// The backward's checks and launches.  x is the saved input, or with x_scales
+// the codes of its 8-bit checkpoint (then u is required).
+static qlora_status run_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s, const void* x,
+                            const uint8_t* x_scales, const qlora_bf16* g, const uint8_t* codes,
+                            const uint8_t* absmax8, const float* c2, const qlora_bf16* A, const qlora_bf16* B,
+                            const float* u, qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
+                            const qlora_dropout* dropout, bool ckpt, void* workspace, size_t workspace_bytes,
+                            qlora_stream_t stream) {
   qlora_status st = check_linear(M, n, m, r, s);
   if (st != QLORA_OK) return st;
   DropoutDev dd;
@@ -746,9 +759,10 @@ qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, flo
   if (st != QLORA_OK) return st;
   const bool drop = dd.on != 0;
   if (!x || !g || !codes || !absmax8 || !c2 || !A || !B || !grad_A || !grad_B) return QLORA_ERR_NULL;
+  if (ckpt && (!x_scales || !u)) return QLORA_ERR_NULL;
   if (!aligned16(x) || !aligned16(g) || !aligned16(codes) || !aligned16(absmax8) || !aligned16(c2) ||
       !aligned16(A) || !aligned16(B) || !aligned16(grad_A) || !aligned16(grad_B) || (u && !aligned16(u)) ||
-      (grad_x && !aligned16(grad_x)))
+      (grad_x && !aligned16(grad_x)) || (ckpt && !aligned16(x_scales)))
     return QLORA_ERR_ALIGN;
   const BwdWs w = bwd_ws(M, n, m, r, drop);
   if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
@@ -766,7 +780,7 @@ qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, flo
   const float* uu = u;
   if (!uu) {
     Timed tm("down_proj", hs);
-    launch_down_proj(x, M, n, A, r, part, w.su, at<float>(workspace, w.u), hs, &dd, inv_keep);
+    launch_down_proj(static_cast<const uint16_t*>(x), M, n, A, r, part, w.su, at<float>(workspace, w.u), hs, &dd, inv_keep);
     uu = at<float>(workspace, w.u);
   }
   float* v = at<float>(workspace, w.v);
@@ -806,7 +820,12 @@ qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, flo
     // grad_A = s v^T x_d with x_d = (x * keep) / (1 - p); then the split
     // sums of grad_B and grad_A in one launch, which also clears the grad_x
     // GEMM's hand-off words
-    launch_token_grad(x, M, n, v, r, w.sa, at<float>(workspace, w.gA), hs, &dd, vplanes, true);
+    if (ckpt)
+      launch_token_grad_ckpt(static_cast<const uint8_t*>(x), x_scales, M, n, v, r, w.sa, at<float>(workspace, w.gA),
+                             hs, dd);
+    else
+      launch_token_grad(static_cast<const uint16_t*>(x), M, n, v, r, w.sa, at<float>(workspace, w.gA), hs, &dd,
+                        vplanes, true);
     const SyncZero z = gemm_split_sync(M, n, w.m_pad, ksplit);
     if (w.gpass)
       launch_reduce_grads(at<float>(workspace, w.gbpart), gpass_splits_t(M), mk, m, s, grad_B,
@@ -834,6 +853,35 @@ qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, flo
     }
   }
   return hip_status();
+}
+
+qlora_status qlora_linear_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
+                              const qlora_bf16* g, const uint8_t* codes, const uint8_t* absmax8, const float* c2,
+                              const qlora_bf16* A, const qlora_bf16* B, const float* u, qlora_bf16* grad_x,
+                              qlora_bf16* grad_A, qlora_bf16* grad_B, void* workspace, size_t workspace_bytes,
+                              qlora_stream_t stream) {
+  return qlora_linear_bwd_ex(M, n, m, r, s, x, g, codes, absmax8, c2, A, B, u, grad_x, grad_A, grad_B, nullptr,
+                             workspace, workspace_bytes, stream);
+}
+
+qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
+                                 const qlora_bf16* g, const uint8_t* codes, const uint8_t* absmax8,
+                                 const float* c2, const qlora_bf16* A, const qlora_bf16* B, const float* u,
+                                 qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
+                                 const qlora_dropout* dropout, void* workspace, size_t workspace_bytes,
+                                 qlora_stream_t stream) {
+  return run_bwd(M, n, m, r, s, x, nullptr, g, codes, absmax8, c2, A, B, u, grad_x, grad_A, grad_B, dropout, false,
+                 workspace, workspace_bytes, stream);
+}
+
+qlora_status qlora_linear_bwd_ckpt(int64_t M, int64_t n, int64_t m, int32_t r, float s, const int8_t* x_codes,
+                                   const uint8_t* x_scales, const qlora_bf16* g, const uint8_t* codes,
+                                   const uint8_t* absmax8, const float* c2, const qlora_bf16* A, const qlora_bf16* B,
+                                   const float* u, qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
+                                   const qlora_dropout* dropout, void* workspace, size_t workspace_bytes,
+                                   qlora_stream_t stream) {
+  return run_bwd(M, n, m, r, s, x_codes, x_scales, g, codes, absmax8, c2, A, B, u, grad_x, grad_A, grad_B, dropout,
+                 true, workspace, workspace_bytes, stream);
 }
 
 qlora_status qlora_linear_check(int op, int64_t M, int64_t n, int64_t m, int32_t r, const void* workspace,
@@ -870,6 +918,169 @@ qlora_status qlora_linear_check(int op, int64_t M, int64_t n, int64_t m, int32_t
       hipStreamSynchronize(hs) != hipSuccess)
     return QLORA_ERR_HIP;
   return word ? QLORA_ERR_INCOMPLETE : QLORA_OK;
+}
+
+static qlora_status check_rows(int64_t M, int64_t n) {
+  return M <= 0 || M >= kMaxDim || n <= 0 || n >= ((int64_t)1 << 30) ? QLORA_ERR_SHAPE : QLORA_OK;
+}
+
+qlora_status qlora_checkpoint_pack(int64_t M, int64_t n, const qlora_bf16* x, int8_t* codes, uint8_t* scales,
+                                   qlora_stream_t stream) {
+  const qlora_status st = check_rows(M, n);
+  if (st != QLORA_OK) return st;
+  if (!x || !codes || !scales) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("checkpoint_pack", hs);
+    launch_checkpoint_pack(M, n, x, codes, scales, hs);
+  }
+  return hip_status();
+}
+
+qlora_status qlora_checkpoint_unpack(int64_t M, int64_t n, const int8_t* codes, const uint8_t* scales,
+                                     qlora_bf16* x_out, qlora_stream_t stream) {
+  const qlora_status st = check_rows(M, n);
+  if (st != QLORA_OK) return st;
+  if (!codes || !scales || !x_out) return QLORA_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(x_out)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("checkpoint_unpack", hs);
+    launch_checkpoint_unpack(M, n, codes, scales, x_out, hs);
+  }
+  return hip_status();
+}
+
+// Checks shared by both directions of the norm.
+static qlora_status check_norm(int32_t kind, int32_t x_type, int32_t w_type, int64_t M, int64_t n) {
+  if ((kind != QLORA_NORM_LAYER && kind != QLORA_NORM_RMS) || x_type < QLORA_BF16 || x_type > QLORA_CKPT8 ||
+      (w_type != QLORA_BF16 && w_type != QLORA_F32) || (x_type == QLORA_F32 && w_type != QLORA_F32))
+    return QLORA_ERR_VALUE;
+  const qlora_status st = check_rows(M, n);
+  if (st != QLORA_OK) return st;
+  return n > norm_max_width() ? QLORA_ERR_SHAPE : QLORA_OK;
+}
+
+qlora_status qlora_norm_fwd(int32_t kind, int32_t x_type, int32_t w_type, int64_t M, int64_t n, float eps,
+                            const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+                            int8_t* y_codes, uint8_t* y_scales, qlora_stream_t stream) {
+  const qlora_status st = check_norm(kind, x_type, w_type, M, n);
+  if (st != QLORA_OK) return st;
+  if (x_type == QLORA_CKPT8 || !std::isfinite(eps) || eps < 0.0f) return QLORA_ERR_VALUE;
+  if (y_codes && x_type != QLORA_BF16) return QLORA_ERR_VALUE;
+  if (!x || !w || !y || !rstd || (kind == QLORA_NORM_LAYER && !mean) || !y_codes != !y_scales) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(b) || !aligned16(y) || !aligned16(mean) || !aligned16(rstd) ||
+      !aligned16(y_codes) || !aligned16(y_scales))
+    return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  const bool layer = kind == QLORA_NORM_LAYER;
+  {
+    Timed tm("norm_fwd", hs);
+    launch_norm_fwd(layer, x_type, w_type == QLORA_F32, M, n, eps, x, w, b, y, layer ? mean : nullptr, rstd, y_codes,
+                    y_scales, hs);
+  }
+  return hip_status();
+}
+
+size_t qlora_norm_workspace_bytes(int32_t kind, int64_t M, int64_t n, int32_t grads) {
+  if (check_norm(kind, QLORA_BF16, QLORA_BF16, M, n) != QLORA_OK || grads < 0 || grads > 2) return 0;
+  return norm_bwd_ws_bytes(kind == QLORA_NORM_LAYER, M, n, grads);
+}
+
+qlora_status qlora_norm_bwd(int32_t kind, int32_t x_type, int32_t w_type, int64_t M, int64_t n, const void* x,
+                            const uint8_t* x_scales, const void* g, const void* w, const float* mean,
+                            const float* rstd, void* grad_x, void* grad_w, void* grad_b, void* workspace,
+                            size_t workspace_bytes, qlora_stream_t stream) {
+  const qlora_status st = check_norm(kind, x_type, w_type, M, n);
+  if (st != QLORA_OK) return st;
+  const bool layer = kind == QLORA_NORM_LAYER;
+  if (!x || !g || !w || !rstd || !grad_x || (layer && !mean) || (x_type == QLORA_CKPT8 && !x_scales) ||
+      (grad_b && !grad_w))
+    return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(x_scales) || !aligned16(g) || !aligned16(w) || !aligned16(mean) ||
+      !aligned16(rstd) || !aligned16(grad_x) || !aligned16(grad_w) || !aligned16(grad_b))
+    return QLORA_ERR_ALIGN;
+  const int accs = grad_b ? 2 : grad_w ? 1 : 0;
+  if (accs && (!workspace || workspace_bytes < norm_bwd_ws_bytes(layer, M, n, accs))) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("norm_bwd", hs);
+    launch_norm_bwd(layer, x_type, w_type == QLORA_F32, M, n, x, x_scales, g, w, layer ? mean : nullptr, rstd,
+                    grad_x, accs, grad_w, grad_b, static_cast<float*>(workspace), hs);
+  }
+  return hip_status();
+}
+
+static qlora_status check_logits(int32_t type, int64_t T, int64_t V) {
+  if (type != QLORA_BF16 && type != QLORA_F32) return QLORA_ERR_VALUE;
+  return check_rows(T, V);
+}
+
+size_t qlora_preference_workspace_bytes(int64_t T, int64_t V, int64_t pairs) {
+  if (check_rows(T, V) != QLORA_OK || pairs < 0 || pairs >= ((int64_t)1 << 30)) return 0;
+  return pref_ws_bytes(T, V, pairs);
+}
+
+qlora_status qlora_sequence_logps(int32_t type, int64_t T, int64_t V, int64_t sequences, const void* logits,
+                                  const int64_t* labels, const int32_t* offsets, float* logps, float* lse,
+                                  void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  const qlora_status st = check_logits(type, T, V);
+  if (st != QLORA_OK) return st;
+  if (sequences < 1 || sequences >= kMaxDim) return QLORA_ERR_SHAPE;
+  if (!logits || !labels || !offsets || !logps || !lse) return QLORA_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(labels) || !aligned16(offsets) || !aligned16(logps) || !aligned16(lse))
+    return QLORA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < pref_ws_bytes(T, V, 0)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("preference_fwd", hs);
+    launch_pref_fwd(type, T, V, sequences, 0, logits, labels, offsets, nullptr, 0.0f, 0.0f, nullptr, logps, lse,
+                    nullptr, workspace, hs);
+  }
+  return hip_status();
+}
+
+qlora_status qlora_preference_fwd(int32_t type, int64_t T, int64_t V, int64_t pairs, const void* logits,
+                                  const int64_t* labels, const int32_t* offsets, const float* ref_logps, float beta,
+                                  float label_smoothing, float* loss, float* logps, float* lse, float* coef,
+                                  void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  const qlora_status st = check_logits(type, T, V);
+  if (st != QLORA_OK) return st;
+  if (pairs < 1 || pairs >= ((int64_t)1 << 30)) return QLORA_ERR_SHAPE;
+  if (!std::isfinite(beta) || !(label_smoothing >= 0.0f && label_smoothing <= 1.0f)) return QLORA_ERR_VALUE;
+  if (!logits || !labels || !offsets || !loss || !logps || !lse || !coef) return QLORA_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(labels) || !aligned16(offsets) || !aligned16(ref_logps) || !aligned16(loss) ||
+      !aligned16(logps) || !aligned16(lse) || !aligned16(coef))
+    return QLORA_ERR_ALIGN;
+  if (!workspace || workspace_bytes < pref_ws_bytes(T, V, pairs)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("preference_fwd", hs);
+    launch_pref_fwd(type, T, V, 2 * pairs, pairs, logits, labels, offsets, ref_logps, beta, label_smoothing, loss,
+                    logps, lse, coef, workspace, hs);
+  }
+  return hip_status();
+}
+
+qlora_status qlora_preference_bwd(int32_t type, int64_t T, int64_t V, const void* logits, const int64_t* labels,
+                                  const float* lse, const float* coef, float grad_scale, void* grad_logits,
+                                  qlora_stream_t stream) {
+  const qlora_status st = check_logits(type, T, V);
+  if (st != QLORA_OK) return st;
+  if (!std::isfinite(grad_scale)) return QLORA_ERR_VALUE;
+  if (!logits || !labels || !lse || !coef || !grad_logits) return QLORA_ERR_NULL;
+  if (!aligned16(logits) || !aligned16(labels) || !aligned16(lse) || !aligned16(coef) || !aligned16(grad_logits))
+    return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("preference_bwd", hs);
+    launch_pref_grad(type, T, V, logits, labels, lse, coef, grad_scale, grad_logits, hs);
+  }
+  return hip_status();
 }
 
 qlora_status qlora_profile_enable(int on) {

@@ -13,7 +13,9 @@
 // with line-coalesced 16-byte loads (a wave covers 4 rows x 256 B), keeps
 // the next tile's loads in flight in registers while the MFMAs consume the
 // current one, and reads MFMA fragments out of XOR-swizzled LDS rows.
-#include "qlora_common.h"
+#include <type_traits>
+
+#include "rows.h"
 
 namespace qlora {
 
@@ -190,10 +192,13 @@ __device__ __forceinline__ uint32_t swy(int q, int chunk) {
   return (uint32_t)(q * 128 + ((chunk ^ ((q >> 1) & 7)) << 4));
 }
 
-template <int RB>
-__global__ __launch_bounds__(256) void token_grad_kernel(const uint16_t* __restrict__ X, int64_t M, int64_t J,
+template <int RB, bool kCkpt>
+__global__ __launch_bounds__(256) void token_grad_kernel(const void* __restrict__ X,
+                                                         const uint8_t* __restrict__ scales, int64_t M, int64_t J,
                                                          const float* __restrict__ Y, int R,
                                                          float* __restrict__ part, int64_t tc, DropoutDev drop) {
+  // kCkpt: X holds the codes of X's 8-bit checkpoint, restored on the way to LDS
+  using Piece = std::conditional_t<kCkpt, Raw8<kCkpt8>, u32x4>;
   constexpr int PLANE = RB * 16 * 128;
   constexpr int STAGE = tg::XB + 2 * PLANE;
   __shared__ __align__(16) uint8_t lds[2 * STAGE];
@@ -208,16 +213,22 @@ __global__ __launch_bounds__(256) void token_grad_kernel(const uint16_t* __restr
   const int64_t tend = (tbeg + tc < M) ? tbeg + tc : M;
   const int nst = (int)cdiv(tend - tbeg, tg::TT);
 
-  const uint32_t xbytes = (uint32_t)(M * J * 2);
+  const uint32_t xbytes = (uint32_t)(M * J * (kCkpt ? 1 : 2));
+  const uint32_t pitch = kCkpt ? (uint32_t)ckpt_pitch(J) : 0u;
+  const uint32_t sbytes = (uint32_t)M * pitch;
   const uint32_t ybytes = (uint32_t)(M * R * 4);
   const brsrc_t rx = make_rsrc(X, xbytes);
   const brsrc_t ry = make_rsrc(Y, ybytes);
+  const brsrc_t rs = make_rsrc(scales, sbytes);
   const int prow = tid >> 4;
   const int pc = tid & 15;
   const bool jok = j0 + 8 * pc < J;
-  uint32_t xo[4];
+  uint32_t xo[4], so[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) xo[i] = (uint32_t)(((tbeg + 16 * i + prow) * J + j0 + 8 * pc) * 2);
+  for (int i = 0; i < 4; ++i) {
+    xo[i] = (uint32_t)(((tbeg + 16 * i + prow) * J + j0 + 8 * pc) * (kCkpt ? 1 : 2));
+    so[i] = (uint32_t)(tbeg + 16 * i + prow) * pitch + (uint32_t)((j0 + 8 * pc) >> 5);
+  }
   const int ypieces = 16 * R;  // 16-byte pieces of fp32 in one 64-token Y tile
 
   // Planes rows q in [R, 16 RB) are never written by the stages: clear them.
@@ -230,13 +241,18 @@ __global__ __launch_bounds__(256) void token_grad_kernel(const uint16_t* __restr
         u32x4{0u, 0u, 0u, 0u};
   }
 
-  auto load = [&](int st, u32x4(&xr)[4], u32x4(&yr)[RB]) {
+  auto load = [&](int st, Piece(&xr)[4], u32x4(&yr)[RB]) {
     const int64_t tb = tbeg + (int64_t)st * tg::TT;
-    const uint32_t d = (uint32_t)(st * tg::TT * J * 2);
+    const uint32_t d = (uint32_t)(st * tg::TT * J * (kCkpt ? 1 : 2));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool ok = jok && (tb + 16 * i + prow < tend);
-      xr[i] = bload128(rx, ok ? xo[i] + d : xbytes);
+      if constexpr (kCkpt) {
+        xr[i].k = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(rx, (int)(ok ? xo[i] + d : xbytes), 0, 0));
+        xr[i].c = bload8(rs, ok ? so[i] + (uint32_t)(st * tg::TT) * pitch : sbytes);
+      } else {
+        xr[i] = bload128(rx, ok ? xo[i] + d : xbytes);
+      }
     }
     const uint32_t ybase = (uint32_t)(tb * R * 4);
 #pragma unroll
@@ -245,13 +261,20 @@ __global__ __launch_bounds__(256) void token_grad_kernel(const uint16_t* __restr
       yr[i] = bload128(ry, p < ypieces ? ybase + 16 * p : ybytes);
     }
   };
-  auto store = [&](int buf, int st, const u32x4(&xr)[4], const u32x4(&yr)[RB]) {
+  auto store = [&](int buf, int st, const Piece(&xr)[4], const u32x4(&yr)[RB]) {
     uint8_t* base = lds + buf * STAGE;
     const int64_t tb = tbeg + (int64_t)st * tg::TT;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // dropout (adapter input only): X element (t, j) is e = t J + j
-      u32x4 w = xr[i];
+      u32x4 w;
+      if constexpr (kCkpt) {
+        float v[8];
+        raw_to_f32<kCkpt8>(xr[i], v);
+        w = round_bf16x8(v);  // exact
+      } else {
+        w = xr[i];
+      }
       if (drop.on) w = dropout8(drop, (uint64_t)((tb + 16 * i + prow) * J + j0 + 8 * pc), w);
       *reinterpret_cast<u32x4*>(base + swtg(16 * i + prow, pc)) = w;
     }
@@ -316,7 +339,8 @@ __global__ __launch_bounds__(256) void token_grad_kernel(const uint16_t* __restr
     }
   };
 
-  u32x4 xa[4], ya[RB], xb[4], yb[RB];
+  Piece xa[4], xb[4];
+  u32x4 ya[RB], yb[RB];
   load(0, xa, ya);
   if (nst > 1) load(1, xb, yb);
   for (int st = 0; st < nst; st += 2) {
@@ -1246,10 +1270,10 @@ void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, 
   if (drop && drop->on) {
     const DropoutDev d = *drop;
     switch (rank_blocks(R)) {
-      case 1: hipLaunchKernelGGL(token_grad_kernel<1>, grid, dim3(256), 0, stream, X, M, J, Y, R, part, tc, d); break;
-      case 2: hipLaunchKernelGGL(token_grad_kernel<2>, grid, dim3(256), 0, stream, X, M, J, Y, R, part, tc, d); break;
-      case 4: hipLaunchKernelGGL(token_grad_kernel<4>, grid, dim3(256), 0, stream, X, M, J, Y, R, part, tc, d); break;
-      default: hipLaunchKernelGGL(token_grad_kernel<8>, grid, dim3(256), 0, stream, X, M, J, Y, R, part, tc, d); break;
+      case 1: hipLaunchKernelGGL((token_grad_kernel<1, false>), grid, dim3(256), 0, stream, X, nullptr, M, J, Y, R, part, tc, d); break;
+      case 2: hipLaunchKernelGGL((token_grad_kernel<2, false>), grid, dim3(256), 0, stream, X, nullptr, M, J, Y, R, part, tc, d); break;
+      case 4: hipLaunchKernelGGL((token_grad_kernel<4, false>), grid, dim3(256), 0, stream, X, nullptr, M, J, Y, R, part, tc, d); break;
+      default: hipLaunchKernelGGL((token_grad_kernel<8, false>), grid, dim3(256), 0, stream, X, nullptr, M, J, Y, R, part, tc, d); break;
     }
   } else {
     const int64_t Mp = cdiv(M, 64) * 64;
@@ -1261,6 +1285,22 @@ void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, 
       default: hipLaunchKernelGGL((skinny_token_kernel<8, 3>), grid, dim3(256), 0, stream, X, M, J, planes, Mp, R, part, tc); break;
     }
   }
+}
+
+// The same with X given as its 8-bit checkpoint.
+void launch_token_grad_ckpt(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t J, const float* Y, int R,
+                            int splits, float* part, hipStream_t stream, const DropoutDev& drop) {
+  const int64_t tc = cdiv(cdiv(M, splits), tg::TT) * tg::TT;
+  const dim3 grid((unsigned)cdiv(J, tg::JT), (unsigned)splits);
+#define QLORA_TOKEN_CKPT(RB_) \
+  hipLaunchKernelGGL((token_grad_kernel<RB_, true>), grid, dim3(256), 0, stream, codes, scales, M, J, Y, R, part, tc, drop)
+  switch (rank_blocks(R)) {
+    case 1: QLORA_TOKEN_CKPT(1); break;
+    case 2: QLORA_TOKEN_CKPT(2); break;
+    case 4: QLORA_TOKEN_CKPT(4); break;
+    default: QLORA_TOKEN_CKPT(8); break;
+  }
+#undef QLORA_TOKEN_CKPT
 }
 
 // grad_B = bf16(s_b sum of bpart's nb_split [Jb][R] partials) over the

@@ -1,0 +1,73 @@
+// Shared by the norm's forward and backward kernels: how a row is held.
+#pragma once
+
+#include "rows.h"
+
+namespace qlora {
+
+constexpr int64_t kNormMaxWidth = 16384;
+
+// A row is held by NW waves, VPT pieces of 8 values a thread: piece i of
+// thread t is at column 8 (t + 64 NW i).  The smallest shape that holds the
+// row is taken (a row of n values needs 512 NW VPT >= n).
+template <typename F>
+static void norm_shape(int64_t n, F f) {
+  using std::integral_constant;
+#define QLORA_SHAPE(NW_, VPT_) f(integral_constant<int, NW_>{}, integral_constant<int, VPT_>{})
+  if (n <= 512) QLORA_SHAPE(1, 1);
+  else if (n <= 1024) QLORA_SHAPE(2, 1);
+  else if (n <= 2048) QLORA_SHAPE(4, 1);
+  else if (n <= 4096) QLORA_SHAPE(8, 1);
+  else if (n <= 8192) QLORA_SHAPE(8, 2);
+  else QLORA_SHAPE(8, 4);
+#undef QLORA_SHAPE
+}
+
+// Rows of a workgroup: four waves of a row each where one wave holds a row.
+__host__ __device__ constexpr int norm_rows(int nw) { return nw == 1 ? 4 : 1; }
+
+// This thread's pieces of a row (zeros past its end).  The row's last n % 8
+// values come one by one; with fewer than 8 nothing is read as a vector.
+template <int XT, int VPT>
+__device__ __forceinline__ void load_row(const RowSrc& s, int64_t row, int n, int t, int threads,
+                                         Raw8<XT> (&r)[VPT]) {
+  if (n >= 8) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) r[i] = load_raw8<XT>(s, row, n, 8 * (t + threads * i));
+  }
+  if (n & 7) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = 8 * (t + threads * i);
+      if (col < n && col + 8 > n) r[i] = load_tail8<XT>(s, row, n, col, n - col);
+      else if (n < 8) r[i] = Raw8<XT>{};
+    }
+  }
+}
+
+// Sums of K values over the NW waves that share a row; every wave gets them.
+// Calls take the two slots of `red` in turn: a wave writes a slot again only
+// after the barrier of the call between, which no wave reaches before it has
+// read the slot.
+template <int NW, int K>
+__device__ __forceinline__ void row_sums(float (&v)[K], float (&red)[2][K][NW], int& turn, int wave) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) v[k] = wave_sum(v[k]);
+  if constexpr (NW > 1) {
+    auto& slot = red[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) slot[k][wave] = v[k];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      v[k] = slot[k][0];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) v[k] += slot[k][i];
+    }
+  }
+}
+
+}  // namespace qlora

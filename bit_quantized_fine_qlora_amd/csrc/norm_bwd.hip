@@ -1,0 +1,248 @@
+// Backward of the layer norm and RMS norm, with the reduction of the weights'
+// gradients.  With xh = (x - mean) rstd, d = g w, p = sum d xh / n and
+// q = sum d / n (q = 0 for rms), per row:
+//   grad_x = rstd (d - q - xh p)
+// and over the rows grad_w = sum g xh, grad_b = sum g.  A row of x and g stays
+// in registers between the two uses, so each is read once; x may be its 8-bit
+// checkpoint, restored in registers.  The weights' gradients add up in
+// registers too: a workgroup walks many rows, a thread always holding the same
+// columns, and writes one fp32 partial row at its end, which a second small
+// kernel adds up in a fixed order.  Bound by HBM.
+#include "norm.h"
+
+namespace qlora {
+
+struct NormBwdArgs {
+  int layer;  // kLayer kernels also serve rms with a bias: mean = q = 0 then
+  int n;
+  int64_t M;
+  float inv_n;
+  RowSrc x;
+  const void* g;
+  const void* w;
+  const float* mean;
+  const float* rstd;
+  void* gx;
+  float* part;  // [gridDim.x][accs][pitch] fp32 sums of each workgroup's rows
+  int pitch;
+};
+
+// kAcc: also sum grad_w (and, with kLayer, grad_b).
+template <bool kLayer, bool kAcc, int XT, int WT, int NW, int VPT>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormBwdArgs a) {
+  constexpr int GT = XT == kCkpt8 ? kBf16 : XT;
+  constexpr int ACC = kAcc ? (kLayer ? 2 : 1) : 0;
+  constexpr int K = kLayer ? 2 : 1;
+  // the next row's loads go out ahead of this row's sums, except where the
+  // widest rows leave no registers for it
+  constexpr bool kAhead = VPT < 4;
+  __shared__ float red[2][K][NW];
+  constexpr int TPR = 64 * NW;
+  const int wave = (int)threadIdx.x >> 6;
+  const int t = NW == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * norm_rows(NW);
+  const RowSrc gsrc{a.g, nullptr}, wsrc{a.w, nullptr};
+  Raw8<WT> w[VPT];
+  load_row<WT, VPT>(wsrc, 0, a.n, t, TPR, w);
+  float acc[ACC ? ACC : 1][VPT][8];
+#pragma unroll
+  for (int c = 0; c < ACC; ++c)
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[c][i][j] = 0.0f;
+  int turn = 0;
+  int64_t row = (int64_t)blockIdx.x * norm_rows(NW) + (NW == 1 ? wave : 0);
+  Raw8<XT> xn[VPT];
+  Raw8<GT> gn[VPT];
+  if (kAhead && row < a.M) {
+    load_row<XT, VPT>(a.x, row, a.n, t, TPR, xn);
+    load_row<GT, VPT>(gsrc, row, a.n, t, TPR, gn);
+  }
+  for (; row < a.M; row += step) {
+    Raw8<XT> xr[VPT];
+    Raw8<GT> gr[VPT];
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        xr[i] = xn[i];
+        gr[i] = gn[i];
+      }
+      const int64_t ahead = row + step < a.M ? row + step : row;  // unconditional, as in the forward
+      load_row<XT, VPT>(a.x, ahead, a.n, t, TPR, xn);
+      load_row<GT, VPT>(gsrc, ahead, a.n, t, TPR, gn);
+    } else {
+      load_row<XT, VPT>(a.x, row, a.n, t, TPR, xr);
+      load_row<GT, VPT>(gsrc, row, a.n, t, TPR, gr);
+    }
+    const float mean = kLayer && a.layer ? a.mean[row] : 0.0f;
+    const float rstd = a.rstd[row];
+    float s[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) s[k] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float x[8], g[8], wv[8];
+      raw_to_f32<XT>(xr[i], x);
+      raw_to_f32<GT>(gr[i], g);
+      raw_to_f32<WT>(w[i], wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = (kLayer ? x[j] - mean : x[j]) * rstd;
+        const float d = g[j] * wv[j];
+        s[0] = __builtin_fmaf(d, xh, s[0]);
+        if constexpr (kLayer) s[1] += d;
+        if constexpr (ACC > 0) acc[0][i][j] = __builtin_fmaf(g[j], xh, acc[0][i][j]);
+        if constexpr (ACC > 1) acc[1][i][j] += g[j];
+      }
+    }
+    row_sums<NW, K>(s, red, turn, wave);
+    const float p = s[0] * a.inv_n;
+    const float q = kLayer && a.layer ? s[K - 1] * a.inv_n : 0.0f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      float x[8], g[8], wv[8], o[8];
+      raw_to_f32<XT>(xr[i], x);
+      raw_to_f32<GT>(gr[i], g);
+      raw_to_f32<WT>(w[i], wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float xh = (kLayer ? x[j] - mean : x[j]) * rstd;
+        float d = g[j] * wv[j];
+        if constexpr (kLayer) d -= q;
+        o[j] = rstd * (d - xh * p);
+      }
+      store8<GT>(a.gx, row, a.n, 8 * (t + TPR * i), o);
+    }
+  }
+  if constexpr (ACC > 0) {
+    if constexpr (NW == 1) {
+      __shared__ float sum[4][512];  // the four waves' sums, added in wave order
+#pragma unroll
+      for (int c = 0; c < ACC; ++c) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[wave][8 * t + j] = acc[c][0][j];
+        __syncthreads();
+        for (int col = (int)threadIdx.x; col < a.n; col += 256)
+          a.part[((int64_t)blockIdx.x * ACC + c) * a.pitch + col] =
+              ((sum[0][col] + sum[1][col]) + sum[2][col]) + sum[3][col];
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < ACC; ++c)
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+          const int col = 8 * (t + TPR * i);
+          float* dst = a.part + ((int64_t)blockIdx.x * ACC + c) * a.pitch + col;
+          if (col < a.pitch) {
+            *reinterpret_cast<f32x4*>(dst) = f32x4{acc[c][i][0], acc[c][i][1], acc[c][i][2], acc[c][i][3]};
+            *reinterpret_cast<f32x4*>(dst + 4) = f32x4{acc[c][i][4], acc[c][i][5], acc[c][i][6], acc[c][i][7]};
+          }
+        }
+    }
+  }
+}
+
+// grad_w and grad_b: the workgroups' partial rows added up.  Workgroup = 64
+// columns of one of the two: 16 groups of 16 threads take every 16th part
+// each, 4 columns a thread and 8 parts in flight, and the groups' sums are
+// added in group order.
+__global__ __launch_bounds__(256) void norm_param_sum_kernel(const float* __restrict__ part, int parts, int accs,
+                                                             int n, int pitch, int w_f32, void* __restrict__ gw,
+                                                             void* __restrict__ gb) {
+  __shared__ f32x4 sum[16][17];
+  const int tid = (int)threadIdx.x, lane = tid & 15, group = tid >> 4;
+  const int tiles = (n + 63) / 64;
+  const int c = (int)blockIdx.x / tiles;
+  const int col = (int)(blockIdx.x % tiles) * 64 + 4 * lane;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (col < pitch) {
+    for (int k0 = group; k0 < parts; k0 += 16 * 8) {
+      f32x4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int k = k0 + 16 * u < parts ? k0 + 16 * u : group;
+        v[u] = *reinterpret_cast<const f32x4*>(part + ((int64_t)k * accs + c) * pitch + col);
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (k0 + 16 * u < parts) s += v[u];
+    }
+  }
+  sum[group][lane] = s;
+  __syncthreads();
+  if (tid < 64) {
+    const int o = (int)(blockIdx.x % tiles) * 64 + tid;
+    if (o < n) {
+      float v = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v += sum[k][tid >> 2][tid & 3];
+      void* out = c ? gb : gw;
+      if (w_f32) static_cast<float*>(out)[o] = v;
+      else static_cast<uint16_t*>(out)[o] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+int64_t norm_max_width() { return kNormMaxWidth; }
+
+// Workgroups of the backward pass, each one partial row of each gradient: as
+// many as are resident at once, or what the rows need.
+static int64_t norm_bwd_groups(int64_t M, int64_t n) {
+  int64_t groups = 0;
+  norm_shape(n, [&](auto nw, auto) {
+    constexpr int NW = decltype(nw)::value;
+    const int64_t want = (M + norm_rows(NW) - 1) / norm_rows(NW);
+    const int64_t most = (int64_t)device_cus() * (NW <= 4 ? 4 : NW == 8 ? 2 : 1);
+    groups = want < most ? want : most;
+  });
+  return groups;
+}
+
+static int norm_pitch(int64_t n) { return (int)((n + 7) / 8 * 8); }
+
+// Gradients that the kernels sum: the layer norm's kernel sums both or none.
+static int norm_sums(int layer, int accs) { return accs == 0 ? 0 : layer ? 2 : accs; }
+
+size_t norm_bwd_ws_bytes(int layer, int64_t M, int64_t n, int accs) {
+  return (size_t)norm_bwd_groups(M, n) * (size_t)norm_sums(layer, accs) * (size_t)norm_pitch(n) * sizeof(float);
+}
+
+template <bool kLayer, bool kAcc, int XT, int WT>
+static void norm_bwd_shaped(const NormBwdArgs& a, hipStream_t stream) {
+  norm_shape(a.n, [&](auto nw, auto vpt) {
+    constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
+    hipLaunchKernelGGL((norm_bwd_kernel<kLayer, kAcc, XT, WT, NW, VPT>), dim3((unsigned)norm_bwd_groups(a.M, a.n)),
+                       dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);
+  });
+}
+
+template <int XT, int WT>
+static void norm_bwd_typed(const NormBwdArgs& a, int sums, hipStream_t stream) {
+  if (a.layer || sums == 2)
+    sums ? norm_bwd_shaped<true, true, XT, WT>(a, stream) : norm_bwd_shaped<true, false, XT, WT>(a, stream);
+  else
+    sums ? norm_bwd_shaped<false, true, XT, WT>(a, stream) : norm_bwd_shaped<false, false, XT, WT>(a, stream);
+}
+
+// accs: 0 none of the weights' gradients, 1 grad_w, 2 grad_w and grad_b.
+void launch_norm_bwd(int layer, int x_type, int w_f32, int64_t M, int64_t n, const void* x, const uint8_t* x_scales,
+                     const void* g, const void* w, const float* mean, const float* rstd, void* gx, int accs, void* gw,
+                     void* gb, float* part, hipStream_t stream) {
+  const int pitch = norm_pitch(n), sums = norm_sums(layer, accs);
+  const NormBwdArgs a{layer, (int)n, M, 1.0f / (float)n, RowSrc{x, x_scales}, g, w, mean, rstd, gx, part, pitch};
+  if (x_type == kF32) norm_bwd_typed<kF32, kF32>(a, sums, stream);
+  else if (x_type == kBf16) w_f32 ? norm_bwd_typed<kBf16, kF32>(a, sums, stream) : norm_bwd_typed<kBf16, kBf16>(a, sums, stream);
+  else w_f32 ? norm_bwd_typed<kCkpt8, kF32>(a, sums, stream) : norm_bwd_typed<kCkpt8, kBf16>(a, sums, stream);
+  if (accs) {
+    const int tiles = (int)((n + 63) / 64);
+    hipLaunchKernelGGL(norm_param_sum_kernel, dim3((unsigned)(tiles * accs)), dim3(256), 0, stream, part,
+                       (int)norm_bwd_groups(M, n), sums, (int)n, pitch, w_f32, gw, gb);
+  }
+}
+
+}  // namespace qlora

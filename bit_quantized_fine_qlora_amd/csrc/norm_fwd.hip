@@ -1,0 +1,139 @@
+// Layer norm and RMS norm of the rows of an M x n tensor.
+//   layer: mean = sum x / n, rstd = (sum (x - mean)^2 / n + eps)^(-1/2)
+//   rms:   mean = 0,         rstd = (sum x^2 / n + eps)^(-1/2)
+//   y = (x - mean) rstd w + b
+// A row stays in registers between its uses, so x is read from memory once;
+// the variance is the mean of squared differences (a second pass over the
+// registers), not a difference of means.  With a checkpoint asked for, y is
+// also written in 8 bits while it is in registers, which saves the packing
+// kernel's read.  Bound by HBM.
+#include "norm.h"
+
+namespace qlora {
+
+struct NormFwdArgs {
+  int n;
+  int64_t M;
+  float eps, inv_n;
+  const void* x;
+  const void* w;
+  const void* b;  // may be null
+  void* y;
+  float* mean;
+  float* rstd;
+  int8_t* codes;  // checkpoint of y, may be null (bf16 only)
+  uint8_t* scales;
+};
+
+// Persistent workgroups walk the rows; the next row's loads go out before
+// the current row is reduced.
+template <bool kLayer, int XT, int WT, int NW, int VPT>
+__global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormFwdArgs a) {
+  __shared__ float red[2][1][NW];
+  int turn = 0;
+  constexpr int TPR = 64 * NW;
+  const int wave = (int)threadIdx.x >> 6;
+  const int t = NW == 1 ? (int)threadIdx.x & 63 : (int)threadIdx.x;
+  const int64_t step = (int64_t)gridDim.x * norm_rows(NW);
+  const RowSrc src{a.x, nullptr};
+  int64_t row = (int64_t)blockIdx.x * norm_rows(NW) + (NW == 1 ? wave : 0);
+  if (row >= a.M) return;  // a whole workgroup, or (NW = 1, no barriers) a wave
+  Raw8<WT> w[VPT];
+  load_row<WT, VPT>(RowSrc{a.w, nullptr}, 0, a.n, t, TPR, w);
+  Raw8<XT> next[VPT];
+  load_row<XT, VPT>(src, row, a.n, t, TPR, next);
+  for (; row < a.M; row += step) {
+    Raw8<XT> r[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) r[i] = next[i];
+    // unconditional (see load_raw8); after the last row this row again, from the cache
+    load_row<XT, VPT>(src, row + step < a.M ? row + step : row, a.n, t, TPR, next);
+    float mean = 0.0f;
+    if constexpr (kLayer) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        float v[8];
+        raw_to_f32<XT>(r[i], v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] += v[j];
+      }
+      row_sums<NW, 1>(s, red, turn, wave);
+      mean = s[0] * a.inv_n;
+    }
+    float s[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = 8 * (t + TPR * i);
+      float v[8];
+      raw_to_f32<XT>(r[i], v);
+      float q = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float d = v[j];
+        if constexpr (kLayer) d = col + j < a.n ? d - mean : 0.0f;
+        q = __builtin_fmaf(d, d, q);
+      }
+      s[0] += q;
+    }
+    row_sums<NW, 1>(s, red, turn, wave);
+    const float rstd = 1.0f / __builtin_sqrtf(s[0] * a.inv_n + a.eps);
+    if (t == 0) {
+      a.rstd[row] = rstd;
+      if constexpr (kLayer) a.mean[row] = mean;
+    }
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int col = 8 * (t + TPR * i);
+      float v[8], wv[8];
+      raw_to_f32<XT>(r[i], v);
+      raw_to_f32<WT>(w[i], wv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = (kLayer ? v[j] - mean : v[j]) * rstd * wv[j];
+      if (a.b) {
+        Raw8<WT> b[1];
+        float bv[8];
+        load_row<WT, 1>(RowSrc{a.b, nullptr}, 0, a.n, t + TPR * i, 0, b);
+        raw_to_f32<WT>(b[0], bv);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += bv[j];
+      }
+      store8<XT>(a.y, row, a.n, col, v);
+      if constexpr (XT == kBf16) {
+        if (a.codes) {
+          // past the row's end w and b are zeros, but 0 times a non-finite
+          // mean or rstd is not
+          u32x4 y = round_bf16x8(v);
+          if (col + 8 > a.n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (col + j >= a.n) y[j >> 1] &= (j & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+          }
+          ckpt_store8(a.codes, a.scales, row, a.n, col, y);
+        }
+      }
+    }
+  }
+}
+
+template <bool kLayer, int XT, int WT>
+static void norm_fwd_typed(const NormFwdArgs& a, hipStream_t stream) {
+  norm_shape(a.n, [&](auto nw, auto vpt) {
+    constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
+    const int64_t wgs = (a.M + norm_rows(NW) - 1) / norm_rows(NW);
+    const int64_t most = (int64_t)device_cus() * (NW <= 4 ? 8 : NW == 8 ? 4 : 2);
+    hipLaunchKernelGGL((norm_fwd_kernel<kLayer, XT, WT, NW, VPT>), dim3((unsigned)(wgs < most ? wgs : most)),
+                       dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);
+  });
+}
+
+void launch_norm_fwd(int layer, int x_type, int w_f32, int64_t M, int64_t n, float eps, const void* x, const void* w,
+                     const void* b, void* y, float* mean, float* rstd, int8_t* codes, uint8_t* scales,
+                     hipStream_t stream) {
+  const NormFwdArgs a{(int)n, M, eps, 1.0f / (float)n, x, w, b, y, mean, rstd, codes, scales};
+  if (x_type == kF32) layer ? norm_fwd_typed<true, kF32, kF32>(a, stream) : norm_fwd_typed<false, kF32, kF32>(a, stream);
+  else if (w_f32) layer ? norm_fwd_typed<true, kBf16, kF32>(a, stream) : norm_fwd_typed<false, kBf16, kF32>(a, stream);
+  else layer ? norm_fwd_typed<true, kBf16, kBf16>(a, stream) : norm_fwd_typed<false, kBf16, kBf16>(a, stream);
+}
+
+}  // namespace qlora

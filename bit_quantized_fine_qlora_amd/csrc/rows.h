@@ -1,0 +1,274 @@
+// Pieces shared by the row-wise training operators (norm, 8-bit checkpoints,
+// preference loss): 8 values of a row in registers, the 8-bit checkpoint
+// format, and sums over a workgroup.
+//
+// Rows have any length, so a row's 8-value pieces need not be 16-byte
+// aligned; global memory takes vector accesses at any alignment of the
+// element, and the types below only tell the compiler so.
+#pragma once
+
+#include <type_traits>
+
+#include "qlora_common.h"
+
+namespace qlora {
+
+// types of a row operand, as the C ABI numbers them
+constexpr int kBf16 = 0, kF32 = 1, kCkpt8 = 2;
+
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef u32x2 u32x2_any __attribute__((aligned(1)));
+
+// Length of a checkpoint's row of scale bytes: one per 32 values, rounded up
+// to a multiple of 4 (the bytes past ceil(n / 32) are zero).
+__host__ __device__ static inline int64_t ckpt_pitch(int64_t n) { return (n + 127) / 128 * 4; }
+
+// ---------------------------------------------------------------------------
+// 8 values in registers, as they were loaded
+// ---------------------------------------------------------------------------
+template <int XT>
+struct Raw8;
+template <>
+struct Raw8<kBf16> {
+  u32x4 w;
+};
+template <>
+struct Raw8<kF32> {
+  f32x4 a, b;
+};
+template <>
+struct Raw8<kCkpt8> {
+  u32x2 k;
+  uint32_t c;
+};
+
+// One row operand: its base and, for a checkpoint, the scale bytes' base.
+struct RowSrc {
+  const void* p;
+  const uint8_t* scales;
+};
+
+// Values col .. col + 7 of a row, all of which the row has.
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load_full8(const RowSrc& s, int64_t row, int n, int col) {
+  const int64_t e = row * n + col;
+  Raw8<XT> r;
+  if constexpr (XT == kBf16) {
+    r.w = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(s.p) + e);
+  } else if constexpr (XT == kF32) {
+    const float* p = static_cast<const float*>(s.p) + e;
+    r.a = *reinterpret_cast<const f32x4_any*>(p);
+    r.b = *reinterpret_cast<const f32x4_any*>(p + 4);
+  } else {
+    r.k = *reinterpret_cast<const u32x2_any*>(static_cast<const uint8_t*>(s.p) + e);
+    r.c = s.scales[row * ckpt_pitch(n) + (col >> 5)];
+  }
+  return r;
+}
+
+// The same, or zeros unless all 8 lie in the row.  The load is unconditional
+// (a piece that does not fit reads the row's first 8 values instead, so n
+// must be at least 8): a load under a branch would make the compiler wait for
+// every load in flight where the paths meet.
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load_raw8(const RowSrc& s, int64_t row, int n, int col) {
+  const bool ok = col + 8 <= n;
+  Raw8<XT> r = load_full8<XT>(s, row, n, ok ? col : 0);
+  if constexpr (XT == kBf16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r.w[j] = ok ? r.w[j] : 0u;
+  } else if constexpr (XT == kF32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      r.a[j] = ok ? r.a[j] : 0.0f;
+      r.b[j] = ok ? r.b[j] : 0.0f;
+    }
+  } else {
+    r.k[0] = ok ? r.k[0] : 0u;
+    r.k[1] = ok ? r.k[1] : 0u;
+    r.c = ok ? r.c : 0u;
+  }
+  return r;
+}
+
+// The first `count` (1..7) of 8 values from `col` on, the rest zero.
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load_tail8(const RowSrc& s, int64_t row, int n, int col, int count) {
+  const int64_t e = row * n + col;
+  Raw8<XT> r;
+  if constexpr (XT == kBf16) {
+    const uint16_t* p = static_cast<const uint16_t*>(s.p) + e;
+    r.w = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < count) r.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
+  } else if constexpr (XT == kF32) {
+    const float* p = static_cast<const float*>(s.p) + e;
+    r.a = r.b = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < count) (j < 4 ? r.a : r.b)[j & 3] = p[j];
+  } else {
+    const uint8_t* p = static_cast<const uint8_t*>(s.p) + e;
+    r.k = u32x2{0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (j < count) r.k[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
+    r.c = s.scales[row * ckpt_pitch(n) + (col >> 5)];
+  }
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// The 8-bit checkpoint of a bf16 row.  A block of 32 consecutive values keeps
+// 8-bit integers k and one byte c; the value is k 2^(c - 127).  With E the
+// exponent field of the block's largest magnitude, c = max(E, 7) - 6, which
+// puts that magnitude at 64 <= |k| < 128 (below for E < 7: steps under
+// 2^-126 are not used), and k = x 2^(127 - c) rounded half to even and held
+// within +-127.  A power-of-two step costs up to a factor of two against
+// largest / 127, and a block of 32 instead of a row wins more than that back
+// where some channels are far larger than others; in exchange both
+// directions are exact scalings: a restored value is a bf16 number, so a
+// kernel that restores in registers sees the same bits as one that reads the
+// restored tensor, and the 8-bit mantissa of the largest values loses one bit.
+// c = 255 marks a block with an infinity or NaN: k = 0 throughout, and
+// 0 times the infinite scale restores the whole block as NaN.
+// ---------------------------------------------------------------------------
+
+// Codes (4 to a word) and scale byte of 8 bf16 values; 4 lanes that are
+// neighbours in a quad hold one block's 32 values and get the same c.
+__device__ __forceinline__ void ckpt_encode8(const u32x4& w, u32x2& k, uint32_t& c) {
+  typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w[j] & 0x7FFF7FFFu));
+  uint32_t top = m[0] > m[1] ? m[0] : m[1];
+  uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, true);  // quad lanes 1 0 3 2
+  top = top > o ? top : o;
+  o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0x4E, 0xF, 0xF, true);  // quad lanes 2 3 0 1
+  top = top > o ? top : o;
+  const uint32_t e = top >> 7;
+  c = e == 255u ? 255u : (e > 7u ? e : 7u) - 6u;
+  const float inv = __uint_as_float((254u - c) << 23);  // 2^(127 - c)
+  uint32_t b[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = (j & 1) ? bf16_hi_to_f32(w[j >> 1]) : bf16_lo_to_f32(w[j >> 1]);
+    // the product is exact; adding 1.5 2^23 rounds it half to even and leaves
+    // the integer in the sum's low byte
+    b[j] = __float_as_uint(__builtin_amdgcn_fmed3f(x * inv, -127.0f, 127.0f) + 12582912.0f);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    k[h] = __builtin_amdgcn_perm(b[4 * h + 1], b[4 * h], 0x0C0C0400u) |
+           __builtin_amdgcn_perm(b[4 * h + 3], b[4 * h + 2], 0x04000C0Cu);
+  if (c == 255u) k = u32x2{0u, 0u};
+}
+
+__device__ __forceinline__ float ckpt_scale(uint32_t c) { return __uint_as_float(c << 23); }  // 2^(c - 127)
+
+__device__ __forceinline__ float ckpt_int(uint32_t word, int j) { return (float)(int8_t)(word >> (8 * j)); }
+
+template <int XT>
+__device__ __forceinline__ void raw_to_f32(const Raw8<XT>& r, float (&v)[8]) {
+  if constexpr (XT == kBf16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = bf16_lo_to_f32(r.w[j]);
+      v[2 * j + 1] = bf16_hi_to_f32(r.w[j]);
+    }
+  } else if constexpr (XT == kF32) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = r.a[j];
+      v[4 + j] = r.b[j];
+    }
+  } else {
+    const float s = ckpt_scale(r.c);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = s * ckpt_int(r.k[j >> 2], j & 3);
+  }
+}
+
+__device__ __forceinline__ u32x4 round_bf16x8(const float (&v)[8]) {
+  return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+// Stores the first min(8, n - col) of 8 values (none past the row's end),
+// rounded to bf16 where XT is.
+template <int XT>
+__device__ __forceinline__ void store8(void* base, int64_t row, int n, int col, const float (&v)[8]) {
+  if (col >= n) return;
+  const int64_t e = row * n + col;
+  if constexpr (XT == kBf16) {
+    uint16_t* p = static_cast<uint16_t*>(base) + e;
+    const u32x4 w = round_bf16x8(v);
+    if (col + 8 <= n) {
+      *reinterpret_cast<u32x4_any*>(p) = w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (col + j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+  } else {
+    float* p = static_cast<float*>(base) + e;
+    if (col + 8 <= n) {
+      *reinterpret_cast<f32x4_any*>(p) = f32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_any*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (col + j < n) p[j] = v[j];
+    }
+  }
+}
+
+// Encodes and stores 8 bf16 values (zeros past the row's end) of the
+// checkpoint row; the 4 lanes of a quad hold neighbouring pieces, and lanes
+// up to the padded row length take part.
+__device__ __forceinline__ void ckpt_store8(int8_t* codes, uint8_t* scales, int64_t row, int n, int col,
+                                            const u32x4& w) {
+  u32x2 k;
+  uint32_t c;
+  ckpt_encode8(w, k, c);
+  if (col + 8 <= n) {
+    *reinterpret_cast<u32x2_any*>(codes + row * n + col) = k;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 7; ++j)
+      if (col + j < n) codes[row * n + col + j] = (int8_t)(k[j >> 2] >> (8 * (j & 3)));
+  }
+  const int64_t pitch = ckpt_pitch(n);
+  if ((col & 31) == 0 && (col >> 5) < pitch) scales[row * pitch + (col >> 5)] = (uint8_t)(col < n ? c : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// sums
+// ---------------------------------------------------------------------------
+
+// Sum over the wave's 64 lanes by DPP row shifts and broadcasts; every lane
+// gets it.  The order is fixed.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, decltype(rows)::value,
+                                                    0xF, false));
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});  // row_shr:1
+  add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});  // row_shr:2
+  add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});  // row_shr:4
+  add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});  // row_shr:8
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast:15 into rows 1 and 3
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast:31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d, 64);
+  return v;
+}
+
+}  // namespace qlora

@@ -5,7 +5,9 @@
  *   - blockwise NF4 quantization of a frozen weight with double quantization
  *     of the block constants;
  *   - the adapted forward  h = x W'^T + s (x A^T) B^T,  W' = dequant(W0);
- *   - its backward through the frozen 4-bit weight: grad_x, grad_A, grad_B.
+ *   - its backward through the frozen 4-bit weight: grad_x, grad_A, grad_B;
+ * and what stands next to it in a training step: the norm in front of the
+ * layer, its input kept in 8 bits for the backward pass, and a preference loss.
  * Sources are the QLoRA pages cited at each entry point below.
  *
  * Conventions for every call:
@@ -21,7 +23,8 @@
  *     launched, and leave every output untouched.  A failed launch returns
  *     QLORA_ERR_HIP; outputs are then unspecified.
  *   - Inputs must be finite; non-finite weights or activations give
- *     unspecified (but memory-safe) results.
+ *     unspecified (but memory-safe) results, except where an entry says
+ *     what they give.
  *   - Calls that share a workspace must be ordered (same stream, or
  *     synchronized); calls with separate workspaces may overlap.
  */
@@ -46,7 +49,7 @@ typedef enum {
   QLORA_ERR_ALIGN = -4,     /* a device pointer is not 16-byte aligned */
   QLORA_ERR_WORKSPACE = -5, /* workspace NULL or smaller than required */
   QLORA_ERR_HIP = -6,       /* a HIP launch or query failed */
-  QLORA_ERR_VALUE = -7,     /* s is not finite, or an unknown op id */
+  QLORA_ERR_VALUE = -7,     /* s is not finite, or an unknown op, kind or type id */
   QLORA_ERR_INCOMPLETE = -8 /* a kernel's bounded wait ran out (qlora_linear_check) */
 } qlora_status;
 
@@ -402,6 +405,150 @@ qlora_status qlora_linear_bwd_ex(int64_t M, int64_t n, int64_t m, int32_t r, flo
                                  qlora_stream_t stream);
 
 /*
+ * An activation checkpoint in 8 bits: a bf16 M x n tensor kept for the
+ * backward pass at 33/32 bytes a value ("QLoRA: Efficient Fine-Tuning",
+ * memory-layout figure: with the weight in 4 bits and optimizer state for the
+ * adapters only, activations are what is left to shrink).
+ *   codes    device, M x n int8: k in -127 .. 127.
+ *   scales   device, M rows of 4 ceil(n / 128) bytes: one byte c for each 32
+ *            consecutive values of a row, then zeros.
+ * A value is k 2^(c - 127).  With E the bf16 exponent field of the block's
+ * largest magnitude, c = max(E, 7) - 6 and k = x 2^(127 - c) rounded half to
+ * even, held within -127 .. 127; a block with an infinity or a NaN has
+ * c = 255 and k = 0 and restores as NaN.  Restored values are exact bf16
+ * numbers, at most half a step, 2^(c - 128), from the originals: 1/128 of the
+ * block's largest magnitude, or 2^-127 where that is more.  Requires M >= 1
+ * and 1 <= n < 2^30 (any n).
+ */
+qlora_status qlora_checkpoint_pack(int64_t M, int64_t n, const qlora_bf16* x, int8_t* codes, uint8_t* scales,
+                                   qlora_stream_t stream);
+qlora_status qlora_checkpoint_unpack(int64_t M, int64_t n, const int8_t* codes, const uint8_t* scales,
+                                     qlora_bf16* x_out, qlora_stream_t stream);
+
+/*
+ * qlora_linear_bwd_ex with the saved input x given as its 8-bit checkpoint
+ * (x_codes, x_scales as above, of the M x n input): x enters one product,
+ * grad_A = bf16(s v^T x), which restores it on chip.  u must be given (the
+ * forward's u_out; x is not exact enough to recompute it, and u is small).
+ * Everything else, the workspace (op QLORA_OP_BWD, or QLORA_OP_BWD_DROPOUT
+ * when p > 0) and qlora_linear_check included, as for qlora_linear_bwd_ex.
+ */
+qlora_status qlora_linear_bwd_ckpt(int64_t M, int64_t n, int64_t m, int32_t r, float s, const int8_t* x_codes,
+                                   const uint8_t* x_scales, const qlora_bf16* g, const uint8_t* codes,
+                                   const uint8_t* absmax8, const float* c2, const qlora_bf16* A, const qlora_bf16* B,
+                                   const float* u, qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
+                                   const qlora_dropout* dropout, void* workspace, size_t workspace_bytes,
+                                   qlora_stream_t stream);
+
+/* Types of the operands below; QLORA_CKPT8 is an 8-bit checkpoint. */
+#define QLORA_BF16 0
+#define QLORA_F32 1
+#define QLORA_CKPT8 2
+
+/* Norms over the last axis. */
+#define QLORA_NORM_LAYER 0
+#define QLORA_NORM_RMS 1
+
+/*
+ * The norm in front of a block's adapted linear layers, over the rows of an
+ * M x n tensor, in fp32 with one rounding at the end:
+ *   QLORA_NORM_LAYER: mean = sum x / n, rstd = (sum (x - mean)^2 / n + eps)^(-1/2)
+ *   QLORA_NORM_RMS:   mean = 0,         rstd = (sum x^2 / n + eps)^(-1/2)
+ *   y = (x - mean) rstd w + b
+ *   x, y     device, M x n, both bf16 or both fp32 (x_type).
+ *   w, b     device, n values, bf16 or fp32 (w_type; fp32 with an fp32 x); b
+ *            may be NULL.
+ *   mean     device out, M fp32; not written (and may be NULL) for
+ *            QLORA_NORM_RMS.
+ *   rstd     device out, M fp32.
+ *   y_codes, y_scales  device out: the 8-bit checkpoint of y (x_type
+ *            QLORA_BF16 only), the bits qlora_checkpoint_pack gives, written
+ *            in the same pass; both NULL to skip.
+ * Requires M >= 1, 1 <= n <= 16384, eps >= 0 and finite.  y may be x itself.
+ */
+qlora_status qlora_norm_fwd(int32_t kind, int32_t x_type, int32_t w_type, int64_t M, int64_t n, float eps,
+                            const void* x, const void* w, const void* b, void* y, float* mean, float* rstd,
+                            int8_t* y_codes, uint8_t* y_scales, qlora_stream_t stream);
+
+/*
+ * Workspace bytes of qlora_norm_bwd; grads: 0 without grad_w, 1 with grad_w,
+ * 2 with grad_w and grad_b.  0 on invalid arguments, and for grads = 0.
+ */
+size_t qlora_norm_workspace_bytes(int32_t kind, int64_t M, int64_t n, int32_t grads);
+
+/*
+ * Backward of qlora_norm_fwd for the upstream gradient g = dL/dy.  With
+ * xh = (x - mean) rstd, p = sum g w xh / n and q = sum g w / n (q = 0 for
+ * QLORA_NORM_RMS):
+ *   grad_x = rstd (g w - q - xh p)      (M x n, type of g)
+ *   grad_w = sum over rows of g xh      (n, type of w)
+ *   grad_b = sum over rows of g         (n, type of w)
+ *   x        device, M x n of x_type; with QLORA_CKPT8 the codes of its
+ *            checkpoint, whose scales are x_scales (NULL otherwise).
+ *   g, grad_x  device, M x n: fp32 where x is, bf16 otherwise; grad_x may be
+ *            g itself.
+ *   mean, rstd  the forward's outputs (mean unused for QLORA_NORM_RMS).
+ *   grad_w, grad_b  device out; grad_b may be NULL, or both (frozen weights).
+ * The sums over rows go through fp32 partials in the workspace, added in a
+ * fixed order: results are bit-identical run to run.
+ */
+qlora_status qlora_norm_bwd(int32_t kind, int32_t x_type, int32_t w_type, int64_t M, int64_t n, const void* x,
+                            const uint8_t* x_scales, const void* g, const void* w, const float* mean,
+                            const float* rstd, void* grad_x, void* grad_w, void* grad_b, void* workspace,
+                            size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Log-probabilities of packed sequences from their logits, and the preference
+ * loss of pairs of them.  T tokens in all; logits row t predicts labels[t].
+ *   logits   device, T x V, bf16 or fp32 (type).
+ *   labels   device, T int64; a negative label takes its token out (its row
+ *            is not read), a label >= V makes its log-probability NaN.
+ *   offsets  device, sequences + 1 int32, ascending: sequence s is the tokens
+ *            offsets[s] .. offsets[s + 1] - 1 (none: its sum is 0).  Tokens
+ *            outside every sequence count as unscored.  Values outside
+ *            0 .. T are held within it.
+ *   lse      device out, T fp32: log sum exp of each scored row.
+ *   logps    device out, one fp32 per sequence: the sum over its scored
+ *            tokens of logits[t][labels[t]] - lse[t].
+ * Rows are reduced in fp32 with a running maximum, sums over tokens in 64
+ * bits, in a fixed order.  Requires T, V >= 1.  Logits of -infinity have
+ * probability 0; a row with NaN, +infinity or no finite value gives NaN.
+ */
+size_t qlora_preference_workspace_bytes(int64_t T, int64_t V, int64_t pairs);
+qlora_status qlora_sequence_logps(int32_t type, int64_t T, int64_t V, int64_t sequences, const void* logits,
+                                  const int64_t* labels, const int32_t* offsets, float* logps, float* lse,
+                                  void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Preference loss over `pairs` pairs: sequence 2i is preferred to 2i + 1.
+ *   z_i  = beta ((logps[2i] - ref[2i]) - (logps[2i + 1] - ref[2i + 1]))
+ *   loss = mean over pairs of -(1 - e) log sigma(z_i) - e log sigma(-z_i)
+ *   ref_logps  device, 2 pairs fp32: the reference model's log-probabilities
+ *            (qlora_sequence_logps on its logits), or NULL for zeros.
+ *   beta finite; label_smoothing e in [0, 1].
+ *   loss     device out, 1 fp32.      logps, lse: as above.
+ *   coef     device out, T fp32: dloss / dlog-probability of each token (0
+ *            for unscored ones), which the backward reads.
+ * Workspace: qlora_preference_workspace_bytes(T, V, pairs) (pairs 0 for
+ * qlora_sequence_logps).
+ */
+qlora_status qlora_preference_fwd(int32_t type, int64_t T, int64_t V, int64_t pairs, const void* logits,
+                                  const int64_t* labels, const int32_t* offsets, const float* ref_logps, float beta,
+                                  float label_smoothing, float* loss, float* logps, float* lse, float* coef,
+                                  void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Gradient of the loss with respect to the logits, times grad_scale:
+ *   grad[t][v] = grad_scale coef[t] ([v = labels[t]] - exp(logits[t][v] - lse[t]))
+ * and zeros for tokens that are unscored or whose coefficient is 0.  lse and
+ * coef are the forward's.  grad_logits: device out, type and shape of the
+ * logits; may be the logits themselves.
+ */
+qlora_status qlora_preference_bwd(int32_t type, int64_t T, int64_t V, const void* logits, const int64_t* labels,
+                                  const float* lse, const float* coef, float grad_scale, void* grad_logits,
+                                  qlora_stream_t stream);
+
+/*
  * Completion check of the last qlora_linear_fwd / qlora_linear_bwd(_ex)
  * call (op QLORA_OP_FWD, QLORA_OP_BWD or QLORA_OP_BWD_DROPOUT) that used
  * `workspace` with these sizes.  When a GEMM has more output tiles than the
@@ -427,7 +574,8 @@ qlora_status qlora_linear_check(int op, int64_t M, int64_t n, int64_t m, int32_t
  * qlora_profile_query waits for the recorded events of kernel `name`
  * ("quantize", "dequant", "fwd_gemm", "fwd_small", "dgrad_gemm",
  * "down_proj", "token_grad", "transpose", "gpass", "dropout_term", "merge",
- * "adam") and reports the launch
+ * "adam", "checkpoint_pack", "checkpoint_unpack", "norm_fwd", "norm_bwd",
+ * "preference_fwd", "preference_bwd") and reports the launch
  * count and the summed duration in milliseconds (host pointers).
  */
 qlora_status qlora_profile_enable(int on);
