@@ -1,5 +1,6 @@
 // C ABI of the QLoRA adapted-linear library: argument checks, workspace
 // layout, kernel dispatch and optional kernel timing.  Declared in qlora.h.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -66,7 +67,9 @@ int token_grad_splits(int64_t M, int64_t J, int R);
 void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, int R, int splits, float* part,
                        hipStream_t stream, const DropoutDev* drop, uint16_t* planes, bool planes_ready);
 void launch_token_grad_ckpt(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t J, const float* Y, int R,
-                            int splits, float* part, hipStream_t stream, const DropoutDev& drop);
+                            int splits, float* part, hipStream_t stream, const DropoutDev& drop,
+                            const uint16_t* planes);
+int token_grad_ckpt_splits(int64_t M, int64_t J, int R);
 size_t token_planes_bytes(int64_t M, int R);
 void launch_factor_planes(const float* Y, int nsplit, int64_t M, int R, uint16_t* P, float* Yout, const float* Y2,
                           uint16_t* P2, hipStream_t stream);
@@ -324,6 +327,7 @@ FwdWs fwd_ws(int64_t M, int64_t n, int64_t m, int32_t r) {
 struct BwdWs {
   size_t Bt, part_uv, u, v, gA, gB, gpad, vpart, gbpart, dterm, planes, uplanes, ksplit, total;
   int su, sv, sa, sb;
+  int sc;         // token splits of grad_A from a checkpointed input
   bool gpass;     // v and grad_B from one read of g
   bool has_ksplit;
   int64_t m_pad;  // row length of g as the kernels read it
@@ -340,6 +344,7 @@ BwdWs bwd_ws(int64_t M, int64_t n, int64_t m, int32_t r, bool dropout = false) {
   w.su = down_proj_splits(M, n, r);
   w.sv = down_proj_splits(M, w.m_pad, r);
   w.sa = token_grad_splits(M, n, r);
+  w.sc = token_grad_ckpt_splits(M, n, r);
   w.sb = token_grad_splits(M, w.m_pad, r);
   w.gpass = gpass_supported(r);
   // B^T for v = g B, except where the stream reads B itself
@@ -348,7 +353,7 @@ BwdWs bwd_ws(int64_t M, int64_t n, int64_t m, int32_t r, bool dropout = false) {
   w.part_uv = L.take((size_t)suv * M * r * sizeof(float));
   w.u = L.take((size_t)M * r * sizeof(float));
   w.v = L.take((size_t)M * r * sizeof(float));
-  w.gA = L.take((size_t)w.sa * n * r * sizeof(float));
+  w.gA = L.take((size_t)std::max(w.sa, w.sc) * n * r * sizeof(float));
   w.gB = w.gpass ? 0 : L.take((size_t)w.sb * w.m_pad * r * sizeof(float));
   w.vpart = w.gpass ? L.take((size_t)gpass_splits_f(M, w.m_pad, r) * M * r * sizeof(float)) : 0;
   w.gbpart = w.gpass ? L.take((size_t)gpass_splits_t(M) * w.m_pad * r * sizeof(float)) : 0;
@@ -760,6 +765,8 @@ static qlora_status run_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s,
   const bool drop = dd.on != 0;
   if (!x || !g || !codes || !absmax8 || !c2 || !A || !B || !grad_A || !grad_B) return QLORA_ERR_NULL;
   if (ckpt && (!x_scales || !u)) return QLORA_ERR_NULL;
+  // the checkpointed product addresses v's planes with 32-bit offsets
+  if (ckpt && token_planes_bytes(M, r) >= ((size_t)1 << 32)) return QLORA_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(g) || !aligned16(codes) || !aligned16(absmax8) || !aligned16(c2) ||
       !aligned16(A) || !aligned16(B) || !aligned16(grad_A) || !aligned16(grad_B) || (u && !aligned16(u)) ||
       (grad_x && !aligned16(grad_x)) || (ckpt && !aligned16(x_scales)))
@@ -820,18 +827,19 @@ static qlora_status run_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s,
     // grad_A = s v^T x_d with x_d = (x * keep) / (1 - p); then the split
     // sums of grad_B and grad_A in one launch, which also clears the grad_x
     // GEMM's hand-off words
+    const int sa = ckpt && !drop ? w.sc : w.sa;
     if (ckpt)
-      launch_token_grad_ckpt(static_cast<const uint8_t*>(x), x_scales, M, n, v, r, w.sa, at<float>(workspace, w.gA),
-                             hs, dd);
+      launch_token_grad_ckpt(static_cast<const uint8_t*>(x), x_scales, M, n, v, r, sa, at<float>(workspace, w.gA),
+                             hs, dd, vplanes);
     else
       launch_token_grad(static_cast<const uint16_t*>(x), M, n, v, r, w.sa, at<float>(workspace, w.gA), hs, &dd,
                         vplanes, true);
     const SyncZero z = gemm_split_sync(M, n, w.m_pad, ksplit);
     if (w.gpass)
       launch_reduce_grads(at<float>(workspace, w.gbpart), gpass_splits_t(M), mk, m, s, grad_B,
-                          at<float>(workspace, w.gA), w.sa, n, n, s * inv_keep, grad_A, r, hs, z);
+                          at<float>(workspace, w.gA), sa, n, n, s * inv_keep, grad_A, r, hs, z);
     else
-      launch_reduce_grads(at<float>(workspace, w.gB), w.sb, mk, m, s, grad_B, at<float>(workspace, w.gA), w.sa, n, n,
+      launch_reduce_grads(at<float>(workspace, w.gB), w.sb, mk, m, s, grad_B, at<float>(workspace, w.gA), sa, n, n,
                           s * inv_keep, grad_A, r, hs, z);
   }
   if (grad_x) {

@@ -1036,6 +1036,176 @@ __global__ __launch_bounds__(256) void skinny_token_kernel(const uint16_t* __res
   }
 }
 
+// grad_A's product with X given as its 8-bit checkpoint (X: M x J codes, one
+// scale byte per 32 columns): part[split][j][q] = sum_t x[t][j] P[q][t],
+// x = k 2^(c - 127), restored on chip.  The ring of skinny_token_kernel with
+// half the bytes of X, so that the planes' traffic weighs more: a workgroup
+// takes 256 columns, 32 (one scale block) to each of 8 waves, and the planes
+// of a stage (at 64 ranks as many bytes as its codes) serve all of them.  A
+// lane reads 8 tokens of one column with one ds_read_b64_tr_b8; the integer,
+// its product with the power-of-two scale and the rounding to bf16 are all
+// exact, so the MFMA operands are the bits that restoring X to memory would
+// give.  16-byte unit u of token row t sits at slot u ^ (t % 16): the 8 rows
+// of a transposed read and the 1 KB block writes are free of bank conflicts.
+// 8192 x 28672, 64 ranks: 76 us (the same product of the bf16 tensor 105 us,
+// restoring through registers before LDS 263 us).  Its loads alone, with
+// nothing computed, take 66 us: X alone 45 us (the card streams it in 41 us
+// at any tile shape and ring depth), the planes' second stream through the
+// same load path 14 us and the scale words, 4 bytes of a line each, 9 us.
+// Without the products it takes 69 us, without restoring 66 us.  No faster:
+// 16 waves on 512 columns (75 us, twice the partial sums), restoring a stage
+// ahead (87 us: it needs a stage landed early), waves that take products and
+// restoring in opposite order (95 us), non-temporal loads of X (77 us).
+namespace ck {
+constexpr int WAVES = 8;
+constexpr int TJ = 32 * WAVES;  // columns per workgroup
+constexpr int TS = 64;          // tokens per stage
+}  // namespace ck
+
+template <int RB, int NS>
+__global__ __launch_bounds__(64 * ck::WAVES) void skinny_token_ckpt_kernel(const uint8_t* __restrict__ X,
+                                                                           const uint8_t* __restrict__ scales,
+                                                                           int64_t M, int64_t J,
+                                                                           const uint16_t* __restrict__ P, int64_t Mp,
+                                                                           int R, float* __restrict__ part,
+                                                                           int64_t tc) {
+  using ck::TJ;
+  using ck::WAVES;
+  constexpr int XB = ck::TS * TJ;       // 64 token rows
+  constexpr int XPW = XB / 1024 / WAVES;
+  constexpr int PB = RB * 16 * 128;         // one plane: 16 RB rank rows x 64 tokens
+  // 1 KB blocks of both planes per wave (every wave issues the same number
+  // of loads; blocks past the planes read zeros into the padding)
+  constexpr int PPW = 2 * PB / 1024 >= WAVES ? 2 * PB / 1024 / WAVES : 1;
+  constexpr int SB = WAVES * 64;            // scale words of the 64 tokens, for each 4 waves
+  constexpr int STAGE = XB + PPW * WAVES * 1024 + SB;
+  __shared__ __align__(16) uint8_t s0[STAGE];
+  __shared__ __align__(16) uint8_t s1[STAGE];
+  __shared__ __align__(16) uint8_t s2[STAGE];
+  __shared__ __align__(16) uint8_t s3[NS > 3 ? STAGE : 16];
+  uint8_t* const buf4[4] = {s0, s1, s2, s3};
+  uint8_t* buf[NS];
+#pragma unroll
+  for (int i = 0; i < NS; ++i) buf[i] = buf4[i];
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15;
+  const int lq = lane >> 4;
+  const int64_t j0 = (int64_t)blockIdx.x * TJ;
+  const int split = blockIdx.y;
+  const int64_t tbeg = (int64_t)split * tc;
+  const int64_t tend = (tbeg + tc < M) ? tbeg + tc : M;
+  const int nst = (int)cdiv(tend - tbeg, ck::TS);
+  const int len = (int)(tend - tbeg);
+  const uint32_t pitch = (uint32_t)ckpt_pitch(J);
+  const uint32_t xbytes = (uint32_t)(M * J);
+  const uint32_t sbytes = (uint32_t)M * pitch;
+  const uint32_t pbytes = (uint32_t)(2 * (int64_t)R * Mp * 2);
+  const brsrc_t rx = make_rsrc(X, xbytes);
+  const brsrc_t rs = make_rsrc(scales, sbytes);
+  const brsrc_t rp = make_rsrc(P, pbytes);
+  // Offsets of stage 0; a lane that has nothing to load starts past the end
+  // of its tensor (and stays there: tensors are shorter than 2^30 bytes and a
+  // split's offsets grow by less than that).
+  int xrow[XPW];
+  uint32_t xo[XPW], po[PPW];
+#pragma unroll
+  for (int b = 0; b < XPW; ++b) {  // a 1 KB block is 1024 / TJ token rows
+    xrow[b] = (1024 / TJ) * (XPW * wave + b) + lane / (TJ / 16);
+    const int64_t j = j0 + 16 * ((lane & (TJ / 16 - 1)) ^ (xrow[b] & 15));
+    xo[b] = j < J ? (uint32_t)((tbeg + xrow[b]) * J + j) : xbytes;
+  }
+#pragma unroll
+  for (int b = 0; b < PPW; ++b) {  // a 1 KB block is 8 rank rows of 128 B (swy)
+    const int id = WAVES * b + wave;
+    const int pl = id / (2 * RB);
+    const int q = 8 * (id % (2 * RB)) + (lane >> 3);
+    const int c = (lane & 7) ^ ((q >> 1) & 7);
+    po[b] = pl < 2 && q < R ? (uint32_t)((((int64_t)pl * R + q) * Mp + tbeg + 8 * c) * 2) : pbytes;
+  }
+  // this wave's scale byte is byte wave % 4 of a token's word
+  const uint32_t sword = (uint32_t)(j0 >> 5) + 4u * (uint32_t)(wave >> 2);
+  const uint32_t so = sword < pitch && (wave & 3) == 0 ? (uint32_t)(tbeg + lane) * pitch + sword : sbytes;
+  const int sshift = 8 * (wave & 3);
+  constexpr int LMIN = XPW + PPW;
+  auto issue = [&](int s, uint8_t* stg) {
+    const int left = len - s * ck::TS;  // tokens from this stage's first on
+    const uint32_t xs = (uint32_t)s * (uint32_t)(ck::TS * J);
+#pragma unroll
+    for (int b = 0; b < XPW; ++b)
+      dma16(rx, stg + (XPW * wave + b) * 1024, xrow[b] < left ? xo[b] + xs : xbytes);
+    const uint32_t ps = left > 0 ? (uint32_t)s * (2 * ck::TS) : pbytes;
+#pragma unroll
+    for (int b = 0; b < PPW; ++b) dma16(rp, stg + XB + (WAVES * b + wave) * 1024, po[b] + ps);
+    if ((wave & 3) == 0)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          rs, (__attribute__((address_space(3))) void*)(stg + XB + PPW * WAVES * 1024 + 64 * wave), 4,
+          lane < left ? so + (uint32_t)s * (ck::TS * pitch) : sbytes, 0, 0, 0);
+  };
+  f32x4 acc[2][RB];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int c = 0; c < RB; ++c) acc[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto compute = [&](const uint8_t* stg) {
+    u32x4 a[2][2];  // token half kk, column half ib
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const uint8_t* sw = stg + XB + PPW * WAVES * 1024 + 64 * (wave & ~3) + 4 * (32 * kk + 8 * lq);
+      const u32x4 w0 = *reinterpret_cast<const u32x4*>(sw), w1 = *reinterpret_cast<const u32x4*>(sw + 16);
+      float sc[8], of[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sc[e] = ckpt_scale(__builtin_amdgcn_ubfe(e < 4 ? w0[e & 3] : w1[e & 3], sshift, 8));
+        of[e] = -127.0f * sc[e];
+      }
+#pragma unroll
+      for (int ib = 0; ib < 2; ++ib) {
+        // lanes 2 r + c of each 16-lane group address token row r, columns 8 c .. 8 c + 7
+        const int t = 32 * kk + 8 * lq + (lr >> 1);
+        const uint8_t* src = stg + TJ * t + (((2 * wave + ib) ^ (t & 15)) << 4) + 8 * (lr & 1);
+        typedef int i32x2 __attribute__((ext_vector_type(2)));
+        const i32x2 k = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)src);
+        const uint32_t by[2] = {ckpt_biased((uint32_t)k[0]), ckpt_biased((uint32_t)k[1])};
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = ckpt_value(by[e >> 2], e & 3, sc[e], of[e]);
+        a[kk][ib] = round_bf16x8(v);
+      }
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int cb = 0; cb < RB; ++cb) {
+        const uint32_t off = swy(16 * cb + lr, 4 * kk + lq);
+        const u32x4 bh = *reinterpret_cast<const u32x4*>(stg + XB + off);
+        const u32x4 bl = *reinterpret_cast<const u32x4*>(stg + XB + PB + off);
+#pragma unroll
+        for (int ib = 0; ib < 2; ++ib) {
+          acc[ib][cb] = mfma16x16x32(a[kk][ib], bh, acc[ib][cb]);
+          acc[ib][cb] = mfma16x16x32(a[kk][ib], bl, acc[ib][cb]);
+        }
+      }
+  };
+  ring_run<NS, LMIN>(nst, buf, issue, compute);
+
+  // lane holds columns j = 32 w + 16 ib + 4 lq + e, rank q = 16 cb + lr
+  float* dst = part + (int64_t)split * J * R;
+#pragma unroll
+  for (int cb = 0; cb < RB; ++cb) {
+    const int q = 16 * cb + lr;
+    if (q >= R) continue;
+#pragma unroll
+    for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t j = j0 + 32 * wave + 16 * ib + 4 * lq + e;
+        if (j < J) dst[j * R + q] = acc[ib][cb][e];
+      }
+  }
+}
+
 // bf16 hi / lo planes of an fp32 M x R factor, transposed:
 //   P[0][q][t] = bf16(Y[t][q]),  P[1][q][t] = bf16(Y[t][q] - P[0][q][t]),
 // zero for M <= t < Mp.  Grid y = 0 makes the planes of Y = sum of `nsplit`
@@ -1287,18 +1457,52 @@ void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, 
   }
 }
 
-// The same with X given as its 8-bit checkpoint.
+// Token splits of the reduction over a checkpointed X: as token_grad_splits,
+// for workgroups of 256 columns.
+static int ckpt_wgs_per_cu(int R) { return rank_blocks(R) <= 2 ? 2 : 1; }
+int token_grad_ckpt_splits(int64_t M, int64_t J, int R) {
+  const int64_t tiles = cdiv(J, ck::TJ);
+  const int64_t slots = (int64_t)ckpt_wgs_per_cu(R) * device_cus();
+  int64_t want = cdiv(slots, tiles);
+  const int64_t most = cdiv(M, 256);
+  if (want > most) want = most;
+  if (want > 64) want = 64;
+  if (want < 1) want = 1;
+  want = fewest_rounds_splits(tiles, slots, want);
+  return (int)cdiv(M, cdiv(cdiv(M, want), ck::TS) * ck::TS);
+}
+
+// launch_token_grad with X given as its 8-bit checkpoint: unmasked from the
+// planes (ready), masked through token_grad_kernel with `splits` from
+// token_grad_splits.
 void launch_token_grad_ckpt(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t J, const float* Y, int R,
-                            int splits, float* part, hipStream_t stream, const DropoutDev& drop) {
-  const int64_t tc = cdiv(cdiv(M, splits), tg::TT) * tg::TT;
-  const dim3 grid((unsigned)cdiv(J, tg::JT), (unsigned)splits);
+                            int splits, float* part, hipStream_t stream, const DropoutDev& drop,
+                            const uint16_t* planes) {
+  if (drop.on) {
+    const int64_t tc = cdiv(cdiv(M, splits), tg::TT) * tg::TT;
+    const dim3 grid((unsigned)cdiv(J, tg::JT), (unsigned)splits);
 #define QLORA_TOKEN_CKPT(RB_) \
   hipLaunchKernelGGL((token_grad_kernel<RB_, true>), grid, dim3(256), 0, stream, codes, scales, M, J, Y, R, part, tc, drop)
+    switch (rank_blocks(R)) {
+      case 1: QLORA_TOKEN_CKPT(1); break;
+      case 2: QLORA_TOKEN_CKPT(2); break;
+      case 4: QLORA_TOKEN_CKPT(4); break;
+      default: QLORA_TOKEN_CKPT(8); break;
+    }
+#undef QLORA_TOKEN_CKPT
+    return;
+  }
+  const int64_t Mp = cdiv(M, 64) * 64;
+  const int64_t tc = cdiv(cdiv(M, splits), ck::TS) * ck::TS;
+  const dim3 grid((unsigned)cdiv(J, ck::TJ), (unsigned)splits);
+#define QLORA_TOKEN_CKPT(RB_, NS_)                                                                                  \
+  hipLaunchKernelGGL((skinny_token_ckpt_kernel<RB_, NS_>), grid, dim3(64 * ck::WAVES), 0, stream, codes, scales, M, J, \
+                     planes, Mp, R, part, tc)
   switch (rank_blocks(R)) {
-    case 1: QLORA_TOKEN_CKPT(1); break;
-    case 2: QLORA_TOKEN_CKPT(2); break;
-    case 4: QLORA_TOKEN_CKPT(4); break;
-    default: QLORA_TOKEN_CKPT(8); break;
+    case 1: QLORA_TOKEN_CKPT(1, 3); break;
+    case 2: QLORA_TOKEN_CKPT(2, 3); break;
+    case 4: QLORA_TOKEN_CKPT(4, 4); break;
+    default: QLORA_TOKEN_CKPT(8, 3); break;
   }
 #undef QLORA_TOKEN_CKPT
 }

@@ -169,7 +169,14 @@ __device__ __forceinline__ void ckpt_encode8(const u32x4& w, u32x2& k, uint32_t&
 
 __device__ __forceinline__ float ckpt_scale(uint32_t c) { return __uint_as_float(c << 23); }  // 2^(c - 127)
 
-__device__ __forceinline__ float ckpt_int(uint32_t word, int j) { return (float)(int8_t)(word >> (8 * j)); }
+// Restoring 4 codes: a byte of ckpt_biased(word) is k + 127, and k 2^(c - 127)
+// = fma(k + 127, scale, -127 scale), exactly: the unsigned byte conversion
+// runs at full rate where the signed one takes twice as long, and with a bias
+// of 127 the last term is finite for every scale that a finite block has.
+__device__ __forceinline__ uint32_t ckpt_biased(uint32_t word) { return (word ^ 0x80808080u) - 0x01010101u; }
+__device__ __forceinline__ float ckpt_value(uint32_t biased, int j, float scale, float offset) {
+  return __builtin_fmaf((float)((biased >> (8 * j)) & 0xFFu), scale, offset);
+}
 
 template <int XT>
 __device__ __forceinline__ void raw_to_f32(const Raw8<XT>& r, float (&v)[8]) {
@@ -186,9 +193,10 @@ __device__ __forceinline__ void raw_to_f32(const Raw8<XT>& r, float (&v)[8]) {
       v[4 + j] = r.b[j];
     }
   } else {
-    const float s = ckpt_scale(r.c);
+    const float s = ckpt_scale(r.c), o = -127.0f * s;
+    const uint32_t b[2] = {ckpt_biased(r.k[0]), ckpt_biased(r.k[1])};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = s * ckpt_int(r.k[j >> 2], j & 3);
+    for (int j = 0; j < 8; ++j) v[j] = ckpt_value(b[j >> 2], j & 3, s, o);
   }
 }
 
