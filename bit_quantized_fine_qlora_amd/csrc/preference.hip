@@ -10,7 +10,13 @@
 // sequences, so the logits are read twice: once for the row sums, in one pass
 // with a running maximum, and once, element by element, for the gradient.
 // Rows whose label is negative are neither read nor scored; their gradient is
-// written as zeros.  Both passes are bound by HBM.
+// written as zeros.  Both passes are bound by HBM.  8 pairs, 6144 x 131072
+// bf16 logits, 60 % of the tokens scored: rows 172 us (966 MB, 5.6 TB/s),
+// sequences 9 us, gradient 453 us (2.58 GB, 5.7 TB/s; a plain copy moves
+// 5.1-5.3).  The logits' loads carry the non-temporal hint: 188 us and 486 us
+// without.
+#include <algorithm>
+
 #include "rows.h"
 
 namespace qlora {
@@ -52,7 +58,7 @@ struct PrefRowArgs {
   int V;
   const int64_t* labels;
   int splits;      // workgroups to a row
-  int chunk;       // vocabulary entries of each, a multiple of 8
+  int chunk;       // vocabulary entries of each, a multiple of 2048
   MaxSum* part;    // [T][splits], where splits > 1
   float* lse;      // [T]
   float* lp;       // [T]
@@ -74,17 +80,17 @@ __device__ __forceinline__ float logit_at(const void* logits, int64_t t, int V, 
 // lse and lp of a row from its maximum and sum.  A label past the vocabulary
 // gives NaN and reads nothing.
 template <int XT>
-__device__ __forceinline__ void finish_row(const PrefRowArgs& a, int64_t t, int64_t label, MaxSum r) {
+__device__ __forceinline__ float finish_row(const PrefRowArgs& a, int64_t t, int64_t label, MaxSum r) {
   const float lse = r.m + __builtin_logf(r.s);
   a.lse[t] = lse;
-  a.lp[t] = label < a.V ? logit_at<XT>(a.logits, t, a.V, label) - lse : NAN;
+  return label < a.V ? logit_at<XT>(a.logits, t, a.V, label) - lse : NAN;
 }
 
 // Workgroup = one chunk of one row.
 template <int XT>
 __global__ __launch_bounds__(256) void pref_rows_kernel(PrefRowArgs a) {
-  constexpr int U = 4;             // pieces of 8 values in flight per thread
-  constexpr int kPiece = 256 * 8;  // values of the workgroup's pieces
+  constexpr int U = XT == kBf16 ? 4 : 2;  // pieces of 8 values in flight per thread
+  constexpr int kPiece = 256 * 8;         // values of the workgroup's pieces
   __shared__ MaxSum red[4];
   const int tid = (int)threadIdx.x;
   if (blockIdx.x == 0 && tid == 0 && a.ticket) *a.ticket = 0u;
@@ -106,19 +112,24 @@ __global__ __launch_bounds__(256) void pref_rows_kernel(PrefRowArgs a) {
     const int v1 = v0 + a.chunk < a.V ? v0 + a.chunk : a.V;
     MaxSum r{-INFINITY, 0.0f};
     const int full = v0 + (v1 - v0) / 8 * 8;  // whole pieces end here
-    int b = v0 + 8 * tid;
-    for (; b - 8 * tid + kPiece * U <= full; b += kPiece * U) {
+    // batches of U pieces a thread; in the last one the pieces past the end
+    // read the chunk's first piece and count as -inf
+    for (int b0 = v0; b0 < full; b0 += kPiece * U) {
       Raw8<XT> raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_full8<XT>(src, t, a.V, b + kPiece * u);
+      for (int u = 0; u < U; ++u) {
+        const int b = b0 + 8 * tid + kPiece * u;
+        raw[u] = load_full8<XT, true>(src, t, a.V, b < full ? b : v0);
+      }
       float v[8 * U];
 #pragma unroll
       for (int u = 0; u < U; ++u) raw_to_f32<XT>(raw[u], *reinterpret_cast<float(*)[8]>(v + 8 * u));
-      add_values(r, v);
-    }
-    for (; b < full; b += kPiece) {
-      float v[8];
-      raw_to_f32<XT>(load_full8<XT>(src, t, a.V, b), v);
+      if (b0 + kPiece * U > full) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[8 * u + j] = b0 + 8 * tid + kPiece * u < full ? v[8 * u + j] : -INFINITY;
+      }
       add_values(r, v);
     }
     if (full + tid < v1) {
@@ -133,7 +144,7 @@ __global__ __launch_bounds__(256) void pref_rows_kernel(PrefRowArgs a) {
     if (tid == 0) {
       r = join(join(red[0], red[1]), join(red[2], red[3]));
       if (a.splits == 1)
-        finish_row<XT>(a, t, label, r);
+        a.lp[t] = finish_row<XT>(a, t, label, r);
       else
         a.part[item] = r;
     }
@@ -150,10 +161,10 @@ struct PrefSeqArgs {
   const int32_t* offsets;  // [sequences + 1]
   const int64_t* labels;
   const void* logits;
-  int splits;
+  int splits, group;
   const MaxSum* part;
   float* lse;
-  float* lp;
+  float* lp;               // [T], from the row kernel where rows are whole
   float* logps;            // [sequences]
   // pairs only
   const float* ref;        // [sequences], or null (zeros)
@@ -164,69 +175,92 @@ struct PrefSeqArgs {
   uint32_t* ticket;
 };
 
-// log(1 + exp(v))
-__device__ __forceinline__ double softplus(double v) { return (v > 0.0 ? v : 0.0) + log1p(exp(-fabs(v))); }
-
 // Workgroup = one sequence (kPairs false) or one pair of sequences 2i (the
 // preferred one) and 2i + 1: joins the row chunks, adds up the tokens'
 // log-probabilities, and for a pair forms its loss term and the coefficient
-// of each of its tokens.  Sums over tokens are in 64 bits: a margin is a
-// small difference of sums that grow with the sequences' lengths.  The last
-// workgroup to finish adds the pairs' terms in order.
+// of each of its tokens.  Where rows are chunked, `group` lanes (a power of
+// two that covers the chunks, at most a wave) join a token's chunks, so that
+// few tokens of many chunks still wait for memory once.  Sums over tokens are
+// in 64 bits: a margin is a small difference of sums that grow with the
+// sequences' lengths.  The last workgroup to finish adds the pairs' terms in
+// order.
+constexpr int kSeqWaves = 16;
 template <int XT, bool kPairs>
-__global__ __launch_bounds__(256) void pref_seq_kernel(PrefSeqArgs a) {
-  __shared__ double red[4];
+__global__ __launch_bounds__(64 * kSeqWaves) void pref_seq_kernel(PrefSeqArgs a) {
+  __shared__ double red[2][kSeqWaves];
   __shared__ int last;
-  const int tid = (int)threadIdx.x;
-  constexpr int S = kPairs ? 2 : 1;
+  const int tid = (int)threadIdx.x, wave = tid >> 6;
+  constexpr int S = kPairs ? 2 : 1, kThreads = 64 * kSeqWaves;
+  const int sub = tid & (a.group - 1), per_pass = kThreads / a.group;
   PrefRowArgs ra{};
   ra.logits = a.logits;
   ra.V = a.V;
   ra.lse = a.lse;
   ra.lp = a.lp;
+  auto block_sum = [&](double v, double* slot) {
+    v = wave_sum(v);
+    if ((tid & 63) == 0) slot[wave] = v;
+    __syncthreads();
+    double o = slot[0];
+#pragma unroll
+    for (int w = 1; w < kSeqWaves; ++w) o += slot[w];
+    return o;
+  };
+  float only = 0.0f;  // the term of the only pair
   for (int64_t i = blockIdx.x; i < a.count; i += gridDim.x) {
     double lp[S];
     int64_t lo[S], hi[S];
+    const float rc = kPairs && a.ref ? a.ref[2 * i] : 0.0f, rr = kPairs && a.ref ? a.ref[2 * i + 1] : 0.0f;
 #pragma unroll
     for (int k = 0; k < S; ++k) {
       // offsets come from the device: held within the tokens there are
       const int64_t o0 = a.offsets[S * i + k], o1 = a.offsets[S * i + k + 1];
       lo[k] = o0 < 0 ? 0 : o0 < a.T ? o0 : a.T;
       hi[k] = o1 < lo[k] ? lo[k] : o1 < a.T ? o1 : a.T;
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
       double s = 0.0;
-      for (int64_t t = lo[k] + tid; t < hi[k]; t += 256) {
-        if (a.splits > 1) {
-          const int64_t label = a.labels[t];
-          if (scored(label)) {
-            MaxSum r = a.part[t * a.splits];
-            for (int c = 1; c < a.splits; ++c) r = join(r, a.part[t * a.splits + c]);
-            finish_row<XT>(ra, t, label, r);
-          }
+      if (a.splits == 1) {
+        for (int64_t t = lo[k] + tid; t < hi[k]; t += kThreads) s += (double)a.lp[t];
+      } else {
+        for (int64_t t0 = lo[k]; t0 < hi[k]; t0 += per_pass) {
+          const int64_t t = t0 + tid / a.group;
+          const bool in = t < hi[k];
+          MaxSum r{-INFINITY, 0.0f};
+          const int64_t label = in ? a.labels[t] : -1;
+          if (scored(label))
+            for (int c = sub; c < a.splits; c += a.group) r = join(r, a.part[t * a.splits + c]);
+          for (int d = a.group >> 1; d; d >>= 1) r = join(r, MaxSum{__shfl_xor(r.m, d, 64), __shfl_xor(r.s, d, 64)});
+          if (sub == 0 && scored(label)) s += (double)finish_row<XT>(ra, t, label, r);
         }
-        s += (double)a.lp[t];
       }
-      s = wave_sum(s);
-      __syncthreads();
-      if ((tid & 63) == 0) red[tid >> 6] = s;
-      __syncthreads();
-      lp[k] = ((red[0] + red[1]) + red[2]) + red[3];
+      lp[k] = block_sum(s, red[k]);
       if (tid == 0) a.logps[S * i + k] = (float)lp[k];
     }
     if constexpr (kPairs) {
-      const double rc = a.ref ? (double)a.ref[2 * i] : 0.0, rr = a.ref ? (double)a.ref[2 * i + 1] : 0.0;
-      const double z = (double)a.beta * ((lp[0] - rc) - (lp[1] - rr));
-      const double e = a.smoothing;
-      const double sp = softplus(z), sn = softplus(-z);  // -log sigma(-z), -log sigma(z)
-      // sigma(z) = exp(-sn), sigma(-z) = exp(-sp)
-      const float c = (float)((double)a.beta * (double)a.inv_pairs * (e * exp(-sn) - (1.0 - e) * exp(-sp)));
-      if (tid == 0) a.pair_loss[i] = (float)((1.0 - e) * sn + (e == 0.0 ? 0.0 : e * sp));
+      // 64 bits up to z, whose terms may be large and their difference small;
+      // its logistic function in 32
+      const float z = (float)((double)a.beta * ((lp[0] - rc) - (lp[1] - rr)));
+      const float e = a.smoothing;
+      const float t = expf(-__builtin_fabsf(z)), near = 1.0f / (1.0f + t), far = t / (1.0f + t), l = log1pf(t);
+      const float up = z >= 0.0f ? near : far, down = z >= 0.0f ? far : near;  // sigma(z), sigma(-z)
+      const float su = l + __builtin_fmaxf(-z, 0.0f), sd = l + __builtin_fmaxf(z, 0.0f);  // their -log
+      const float c = a.beta * a.inv_pairs * (e * up - (1.0f - e) * down);
+      only = (1.0f - e) * su + (e == 0.0f ? 0.0f : e * sd);
+      if (tid == 0) a.pair_loss[i] = only;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        for (int64_t t = lo[k] + tid; t < hi[k]; t += 256)
+        for (int64_t t = lo[k] + tid; t < hi[k]; t += kThreads)
           if (scored(a.labels[t])) a.coef[t] = k ? -c : c;
     }
+    __syncthreads();  // red and the rows' log-probabilities have been read
   }
   if constexpr (kPairs) {
+    if (a.count == 1) {
+      if (tid == 0) *a.loss = only;
+      return;
+    }
     if (tid == 0) {
       __threadfence();  // this workgroup's terms before its count
       last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
@@ -235,13 +269,10 @@ __global__ __launch_bounds__(256) void pref_seq_kernel(PrefSeqArgs a) {
     __syncthreads();
     if (last) {
       double s = 0.0;
-      for (int64_t i = tid; i < a.count; i += 256)
+      for (int64_t i = tid; i < a.count; i += kThreads)
         s += (double)__hip_atomic_load(a.pair_loss + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s = wave_sum(s);
-      __syncthreads();
-      if ((tid & 63) == 0) red[tid >> 6] = s;
-      __syncthreads();
-      if (tid == 0) *a.loss = (float)((((red[0] + red[1]) + red[2]) + red[3]) * (double)a.inv_pairs);
+      s = block_sum(s, red[0]);
+      if (tid == 0) *a.loss = (float)(s * (double)a.inv_pairs);
     }
   }
 }
@@ -263,10 +294,10 @@ struct PrefGradArgs {
 
 // Workgroup = one chunk of one row; every element depends on itself alone.
 // Rows go from the last to the first: the forward pass has just left the last
-// ones in the last-level cache.
+// ones in the last-level cache (8 us of the 486 above).
 template <int XT>
 __global__ __launch_bounds__(256) void pref_grad_kernel(PrefGradArgs a) {
-  constexpr int U = 4, kPiece = 256 * 8;
+  constexpr int U = XT == kBf16 ? 4 : 2, kPiece = 256 * 8;
   const int tid = (int)threadIdx.x;
   const RowSrc src{a.logits, nullptr};
   const int64_t items = a.T * a.splits;
@@ -278,10 +309,9 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(PrefGradArgs a) {
     const int64_t label = a.labels[t];
     const float c = scored(label) ? a.coef[t] * a.scale : 0.0f;
     const int full = v0 + (v1 - v0) / 8 * 8;
-    int b = v0 + 8 * tid;
     if (c == 0.0f) {
       const float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (; b < full; b += kPiece) store8<XT>(a.grad, t, a.V, b, z);
+      for (int b = v0 + 8 * tid; b < full; b += kPiece) store8<XT>(a.grad, t, a.V, b, z);
       if (full + tid < v1) {
         if constexpr (XT == kBf16) static_cast<uint16_t*>(a.grad)[t * a.V + full + tid] = 0;
         else static_cast<float*>(a.grad)[t * a.V + full + tid] = 0.0f;
@@ -302,14 +332,19 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(PrefGradArgs a) {
       }
       store8<XT>(a.grad, t, a.V, col, v);
     };
-    for (; b - 8 * tid + kPiece * U <= full; b += kPiece * U) {
+    for (int b0 = v0; b0 < full; b0 += kPiece * U) {
       Raw8<XT> raw[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) raw[u] = load_full8<XT>(src, t, a.V, b + kPiece * u);
+      for (int u = 0; u < U; ++u) {
+        const int col = b0 + 8 * tid + kPiece * u;
+        raw[u] = load_full8<XT, true>(src, t, a.V, col < full ? col : v0);
+      }
 #pragma unroll
-      for (int u = 0; u < U; ++u) grad8(raw[u], b + kPiece * u);
+      for (int u = 0; u < U; ++u) {
+        const int col = b0 + 8 * tid + kPiece * u;
+        if (col < full) grad8(raw[u], col);
+      }
     }
-    for (; b < full; b += kPiece) grad8(load_full8<XT>(src, t, a.V, b), b);
     if (full + tid < v1) {
       const int col = full + tid;
       float v = -c * exp_from(logit_at<XT>(a.logits, t, a.V, col), lse);
@@ -328,17 +363,23 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(PrefGradArgs a) {
 struct PrefSplit {
   int splits, chunk;
 };
-// Chunks of a row: enough workgroups to fill the chip where rows are few, of
-// at least 2048 entries each.
-static PrefSplit pref_split(int64_t T, int64_t V, int64_t want) {
-  int64_t s = (want + T - 1) / T;
-  const int64_t most = (V + 2047) / 2048;
-  if (s > most) s = most;
-  if (s < 1) s = 1;
-  const int64_t chunk = ((V + s - 1) / s + 7) / 8 * 8;
+static PrefSplit pref_chunks(int64_t V, int64_t chunk) {
+  chunk = (chunk + 2047) / 2048 * 2048;
   return PrefSplit{(int)((V + chunk - 1) / chunk), (int)chunk};
 }
-static PrefSplit pref_row_split(int64_t T, int64_t V) { return pref_split(T, V, (int64_t)device_cus() * 4); }
+// Where rows are few, chunks of whole 2048 entries that give every CU four
+// workgroups; one chunk a row otherwise.
+static PrefSplit pref_row_split(int64_t T, int64_t V) {
+  const int64_t want = ((int64_t)device_cus() * 4 + T - 1) / T;
+  return pref_chunks(V, (V + want - 1) / want);
+}
+// The gradient takes chunks of 8192 entries at most: its workgroups write as
+// much as they read, and with short ones the rows that are read and written
+// at a time lie closer together (6144 x 131072 bf16: 453 us in chunks of
+// 6000 to 12000 entries, 486 us by whole rows, 505 us in chunks of 3000).
+static PrefSplit pref_grad_split(int64_t T, int64_t V) {
+  return pref_chunks(V, std::min(pref_row_split(T, V).chunk, 8192));
+}
 
 struct PrefWs {
   size_t part, lp, pair_loss, ticket, total;
@@ -371,22 +412,24 @@ void launch_pref_fwd(int type, int64_t T, int64_t V, int64_t seqs, int64_t pairs
   const dim3 grid(capped(T * p.splits));
   if (type == kBf16) hipLaunchKernelGGL(pref_rows_kernel<kBf16>, grid, dim3(256), 0, stream, r);
   else hipLaunchKernelGGL(pref_rows_kernel<kF32>, grid, dim3(256), 0, stream, r);
-  PrefSeqArgs s{T, (int)V, pairs ? pairs : seqs, offsets, labels, logits, p.splits, r.part, lse, r.lp, logps, ref,
+  int group = 1;
+  while (group < p.splits && group < 64) group *= 2;
+  PrefSeqArgs s{T, (int)V, pairs ? pairs : seqs, offsets, labels, logits, p.splits, group, r.part, lse, r.lp, logps, ref,
                 beta, smoothing, pairs ? 1.0f / (float)pairs : 0.0f, coef,
                 reinterpret_cast<float*>(ws + w.pair_loss), loss, ticket};
   const dim3 sgrid(capped(s.count));
   if (pairs) {
-    if (type == kBf16) hipLaunchKernelGGL((pref_seq_kernel<kBf16, true>), sgrid, dim3(256), 0, stream, s);
-    else hipLaunchKernelGGL((pref_seq_kernel<kF32, true>), sgrid, dim3(256), 0, stream, s);
+    if (type == kBf16) hipLaunchKernelGGL((pref_seq_kernel<kBf16, true>), sgrid, dim3(64 * kSeqWaves), 0, stream, s);
+    else hipLaunchKernelGGL((pref_seq_kernel<kF32, true>), sgrid, dim3(64 * kSeqWaves), 0, stream, s);
   } else {
-    if (type == kBf16) hipLaunchKernelGGL((pref_seq_kernel<kBf16, false>), sgrid, dim3(256), 0, stream, s);
-    else hipLaunchKernelGGL((pref_seq_kernel<kF32, false>), sgrid, dim3(256), 0, stream, s);
+    if (type == kBf16) hipLaunchKernelGGL((pref_seq_kernel<kBf16, false>), sgrid, dim3(64 * kSeqWaves), 0, stream, s);
+    else hipLaunchKernelGGL((pref_seq_kernel<kF32, false>), sgrid, dim3(64 * kSeqWaves), 0, stream, s);
   }
 }
 
 void launch_pref_grad(int type, int64_t T, int64_t V, const void* logits, const int64_t* labels, const float* lse,
                       const float* coef, float scale, void* grad, hipStream_t stream) {
-  const PrefSplit p = pref_split(T, V, (int64_t)device_cus() * 16);
+  const PrefSplit p = pref_grad_split(T, V);
   PrefGradArgs g{logits, T, (int)V, labels, lse, coef, scale, grad, p.splits, p.chunk};
   const dim3 grid(capped(T * p.splits));
   if (type == kBf16) hipLaunchKernelGGL(pref_grad_kernel<kBf16>, grid, dim3(256), 0, stream, g);

@@ -49,19 +49,26 @@ struct RowSrc {
   const uint8_t* scales;
 };
 
+// kNt: with the non-temporal hint, for operands that are read once.
+template <bool kNt, typename T>
+__device__ __forceinline__ T load_as(const void* p) {
+  if constexpr (kNt) return __builtin_nontemporal_load(static_cast<const T*>(p));
+  else return *static_cast<const T*>(p);
+}
+
 // Values col .. col + 7 of a row, all of which the row has.
-template <int XT>
+template <int XT, bool kNt = false>
 __device__ __forceinline__ Raw8<XT> load_full8(const RowSrc& s, int64_t row, int n, int col) {
   const int64_t e = row * n + col;
   Raw8<XT> r;
   if constexpr (XT == kBf16) {
-    r.w = *reinterpret_cast<const u32x4_any*>(static_cast<const uint16_t*>(s.p) + e);
+    r.w = load_as<kNt, u32x4_any>(static_cast<const uint16_t*>(s.p) + e);
   } else if constexpr (XT == kF32) {
     const float* p = static_cast<const float*>(s.p) + e;
-    r.a = *reinterpret_cast<const f32x4_any*>(p);
-    r.b = *reinterpret_cast<const f32x4_any*>(p + 4);
+    r.a = load_as<kNt, f32x4_any>(p);
+    r.b = load_as<kNt, f32x4_any>(p + 4);
   } else {
-    r.k = *reinterpret_cast<const u32x2_any*>(static_cast<const uint8_t*>(s.p) + e);
+    r.k = load_as<kNt, u32x2_any>(static_cast<const uint8_t*>(s.p) + e);
     r.c = s.scales[row * ckpt_pitch(n) + (col >> 5)];
   }
   return r;
@@ -71,10 +78,10 @@ __device__ __forceinline__ Raw8<XT> load_full8(const RowSrc& s, int64_t row, int
 // (a piece that does not fit reads the row's first 8 values instead, so n
 // must be at least 8): a load under a branch would make the compiler wait for
 // every load in flight where the paths meet.
-template <int XT>
+template <int XT, bool kNt = false>
 __device__ __forceinline__ Raw8<XT> load_raw8(const RowSrc& s, int64_t row, int n, int col) {
   const bool ok = col + 8 <= n;
-  Raw8<XT> r = load_full8<XT>(s, row, n, ok ? col : 0);
+  Raw8<XT> r = load_full8<XT, kNt>(s, row, n, ok ? col : 0);
   if constexpr (XT == kBf16) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.w[j] = ok ? r.w[j] : 0u;
