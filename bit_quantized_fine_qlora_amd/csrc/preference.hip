@@ -14,7 +14,7 @@
 // bf16 logits, 60 % of the tokens scored: rows 172 us (966 MB, 5.6 TB/s),
 // sequences 9 us, gradient 453 us (2.58 GB, 5.7 TB/s; a plain copy moves
 // 5.1-5.3).  The logits' loads carry the non-temporal hint: 188 us and 486 us
-// without.
+// without.  5 pairs, 1501 x 50021 fp32: 48 us (180 MB) and 74 us (480 MB).
 #include <algorithm>
 
 #include "rows.h"
@@ -89,8 +89,8 @@ __device__ __forceinline__ float finish_row(const PrefRowArgs& a, int64_t t, int
 // Workgroup = one chunk of one row.
 template <int XT>
 __global__ __launch_bounds__(256) void pref_rows_kernel(PrefRowArgs a) {
-  constexpr int U = XT == kBf16 ? 4 : 2;  // pieces of 8 values in flight per thread
-  constexpr int kPiece = 256 * 8;         // values of the workgroup's pieces
+  constexpr int U = 4;             // pieces of 8 values in flight per thread
+  constexpr int kPiece = 256 * 8;  // values of the workgroup's pieces
   __shared__ MaxSum red[4];
   const int tid = (int)threadIdx.x;
   if (blockIdx.x == 0 && tid == 0 && a.ticket) *a.ticket = 0u;
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void pref_rows_kernel(PrefRowArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int b = b0 + 8 * tid + kPiece * u;
-        raw[u] = load_full8<XT, true>(src, t, a.V, b < full ? b : v0);
+        raw[u] = load_full8<XT, XT == kBf16>(src, t, a.V, b < full ? b : v0);
       }
       float v[8 * U];
 #pragma unroll
@@ -297,7 +297,7 @@ struct PrefGradArgs {
 // ones in the last-level cache (8 us of the 486 above).
 template <int XT>
 __global__ __launch_bounds__(256) void pref_grad_kernel(PrefGradArgs a) {
-  constexpr int U = XT == kBf16 ? 4 : 2, kPiece = 256 * 8;
+  constexpr int U = 4, kPiece = 256 * 8;
   const int tid = (int)threadIdx.x;
   const RowSrc src{a.logits, nullptr};
   const int64_t items = a.T * a.splits;
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256) void pref_grad_kernel(PrefGradArgs a) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int col = b0 + 8 * tid + kPiece * u;
-        raw[u] = load_full8<XT, true>(src, t, a.V, col < full ? col : v0);
+        raw[u] = load_full8<XT, XT == kBf16>(src, t, a.V, col < full ? col : v0);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -373,10 +373,11 @@ static PrefSplit pref_row_split(int64_t T, int64_t V) {
   const int64_t want = ((int64_t)device_cus() * 4 + T - 1) / T;
   return pref_chunks(V, (V + want - 1) / want);
 }
-// The gradient takes chunks of 8192 entries at most: its workgroups write as
-// much as they read, and with short ones the rows that are read and written
-// at a time lie closer together (6144 x 131072 bf16: 453 us in chunks of
-// 6000 to 12000 entries, 486 us by whole rows, 505 us in chunks of 3000).
+// The gradient takes chunks of 8192 entries at most, one batch of loads a
+// workgroup: it writes as much as it reads, and with short workgroups the
+// rows that are read and written at a time lie closer together (6144 x 131072
+// bf16: 453 us in chunks of 6000 to 12000 entries, 486 us by whole rows, 505
+// us in chunks of 3000; 1501 x 50021 fp32: 74 us, 116 us in chunks of 16384).
 static PrefSplit pref_grad_split(int64_t T, int64_t V) {
   return pref_chunks(V, std::min(pref_row_split(T, V).chunk, 8192));
 }

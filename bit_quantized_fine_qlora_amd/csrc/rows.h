@@ -18,6 +18,8 @@ constexpr int kBf16 = 0, kF32 = 1, kCkpt8 = 2;
 
 typedef u32x4 u32x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef f32x8 f32x8_any __attribute__((aligned(4)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 
 // Length of a checkpoint's row of scale bytes: one per 32 values, rounded up
@@ -35,7 +37,7 @@ struct Raw8<kBf16> {
 };
 template <>
 struct Raw8<kF32> {
-  f32x4 a, b;
+  f32x8 v;
 };
 template <>
 struct Raw8<kCkpt8> {
@@ -49,7 +51,10 @@ struct RowSrc {
   const uint8_t* scales;
 };
 
-// kNt: with the non-temporal hint, for operands that are read once.
+// kNt: with the non-temporal hint, for operands that are read once.  Not for
+// fp32, whose 8 values are two loads: the hint drops the line between them
+// (1501 x 50021 logits: loss 56 us with it and 50 us without, gradient 98 and
+// 83 us).
 template <bool kNt, typename T>
 __device__ __forceinline__ T load_as(const void* p) {
   if constexpr (kNt) return __builtin_nontemporal_load(static_cast<const T*>(p));
@@ -64,9 +69,7 @@ __device__ __forceinline__ Raw8<XT> load_full8(const RowSrc& s, int64_t row, int
   if constexpr (XT == kBf16) {
     r.w = load_as<kNt, u32x4_any>(static_cast<const uint16_t*>(s.p) + e);
   } else if constexpr (XT == kF32) {
-    const float* p = static_cast<const float*>(s.p) + e;
-    r.a = load_as<kNt, f32x4_any>(p);
-    r.b = load_as<kNt, f32x4_any>(p + 4);
+    r.v = load_as<kNt, f32x8_any>(static_cast<const float*>(s.p) + e);
   } else {
     r.k = load_as<kNt, u32x2_any>(static_cast<const uint8_t*>(s.p) + e);
     r.c = s.scales[row * ckpt_pitch(n) + (col >> 5)];
@@ -74,27 +77,39 @@ __device__ __forceinline__ Raw8<XT> load_full8(const RowSrc& s, int64_t row, int
   return r;
 }
 
-// The same, or zeros unless all 8 lie in the row.  The load is unconditional
-// (a piece that does not fit reads the row's first 8 values instead, so n
-// must be at least 8): a load under a branch would make the compiler wait for
-// every load in flight where the paths meet.
-template <int XT, bool kNt = false>
-__device__ __forceinline__ Raw8<XT> load_raw8(const RowSrc& s, int64_t row, int n, int col) {
-  const bool ok = col + 8 <= n;
-  Raw8<XT> r = load_full8<XT, kNt>(s, row, n, ok ? col : 0);
+// The same for a piece that may cross or lie past the row's end, in two parts.
+// load_piece8 always loads: a load under a branch would make the compiler wait
+// for every load in flight where the paths meet.  A piece that crosses the end
+// reads the row's last 8 values, one past it the first 8 (so n must be at
+// least 8); finish_piece8, where the values are used, moves the former into
+// place and clears what the row does not have.
+template <int XT>
+__device__ __forceinline__ Raw8<XT> load_piece8(const RowSrc& s, int64_t row, int n, int col) {
+  Raw8<XT> r = load_full8<XT>(RowSrc{s.p, s.scales}, row, n, col + 8 <= n ? col : col < n ? n - 8 : 0);
+  if constexpr (XT == kCkpt8) r.c = s.scales[row * ckpt_pitch(n) + (col < n ? col >> 5 : 0)];
+  return r;
+}
+
+template <int XT>
+__device__ __forceinline__ Raw8<XT> finish_piece8(Raw8<XT> r, int n, int col) {
+  if (col + 8 <= n) return r;
+  const int by = col < n ? col + 8 - n : 8;  // values to move down by
   if constexpr (XT == kBf16) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = ok ? r.w[j] : 0u;
+    u32x4 w = r.w;
+    w = by & 8 ? u32x4{0u, 0u, 0u, 0u} : w;
+    w = by & 4 ? u32x4{w[2], w[3], 0u, 0u} : w;
+    w = by & 2 ? u32x4{w[1], w[2], w[3], 0u} : w;
+    const u32x4 h = {w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16};
+    r.w = by & 1 ? h : w;
   } else if constexpr (XT == kF32) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      r.a[j] = ok ? r.a[j] : 0.0f;
-      r.b[j] = ok ? r.b[j] : 0.0f;
-    }
+    for (int d = 8; d; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) r.v[j] = by & d ? (j + d < 8 ? r.v[(j + d) & 7] : 0.0f) : r.v[j];
   } else {
-    r.k[0] = ok ? r.k[0] : 0u;
-    r.k[1] = ok ? r.k[1] : 0u;
-    r.c = ok ? r.c : 0u;
+    const uint64_t k = by & 8 ? 0ull : ((uint64_t)r.k[1] << 32 | r.k[0]) >> (8 * by);
+    r.k = u32x2{(uint32_t)k, (uint32_t)(k >> 32)};
+    r.c = by & 8 ? 0u : r.c;
   }
   return r;
 }
@@ -112,10 +127,8 @@ __device__ __forceinline__ Raw8<XT> load_tail8(const RowSrc& s, int64_t row, int
       if (j < count) r.w[j >> 1] |= (uint32_t)p[j] << (16 * (j & 1));
   } else if constexpr (XT == kF32) {
     const float* p = static_cast<const float*>(s.p) + e;
-    r.a = r.b = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 7; ++j)
-      if (j < count) (j < 4 ? r.a : r.b)[j & 3] = p[j];
+    for (int j = 0; j < 8; ++j) r.v[j] = j < count ? p[j < count ? j : 0] : 0.0f;
   } else {
     const uint8_t* p = static_cast<const uint8_t*>(s.p) + e;
     r.k = u32x2{0u, 0u};
@@ -195,10 +208,7 @@ __device__ __forceinline__ void raw_to_f32(const Raw8<XT>& r, float (&v)[8]) {
     }
   } else if constexpr (XT == kF32) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = r.a[j];
-      v[4 + j] = r.b[j];
-    }
+    for (int j = 0; j < 8; ++j) v[j] = r.v[j];
   } else {
     const float s = ckpt_scale(r.c), o = -127.0f * s;
     const uint32_t b[2] = {ckpt_biased(r.k[0]), ckpt_biased(r.k[1])};
@@ -212,30 +222,54 @@ __device__ __forceinline__ u32x4 round_bf16x8(const float (&v)[8]) {
 }
 
 // Stores the first min(8, n - col) of 8 values (none past the row's end),
-// rounded to bf16 where XT is.
+// rounded to bf16 where XT is; a piece that crosses the end goes out as 4, 2
+// and 1 values.
 template <int XT>
 __device__ __forceinline__ void store8(void* base, int64_t row, int n, int col, const float (&v)[8]) {
+  typedef uint32_t u32_any __attribute__((aligned(2)));
+  typedef u32x2 u32x2_b __attribute__((aligned(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef f32x2 f32x2_any __attribute__((aligned(4)));
   if (col >= n) return;
   const int64_t e = row * n + col;
   if constexpr (XT == kBf16) {
     uint16_t* p = static_cast<uint16_t*>(base) + e;
-    const u32x4 w = round_bf16x8(v);
+    u32x4 w = round_bf16x8(v);
     if (col + 8 <= n) {
       *reinterpret_cast<u32x4_any*>(p) = w;
     } else {
-#pragma unroll
-      for (int j = 0; j < 7; ++j)
-        if (col + j < n) p[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+      if ((n - col) & 4) {
+        *reinterpret_cast<u32x2_b*>(p) = u32x2{w[0], w[1]};
+        w[0] = w[2];
+        w[1] = w[3];
+        p += 4;
+      }
+      if ((n - col) & 2) {
+        *reinterpret_cast<u32_any*>(p) = w[0];
+        w[0] = w[1];
+        p += 2;
+      }
+      if ((n - col) & 1) *p = (uint16_t)w[0];
     }
   } else {
     float* p = static_cast<float*>(base) + e;
+    f32x4 a = {v[0], v[1], v[2], v[3]};
+    const f32x4 b = {v[4], v[5], v[6], v[7]};
     if (col + 8 <= n) {
-      *reinterpret_cast<f32x4_any*>(p) = f32x4{v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4_any*>(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
+      *reinterpret_cast<f32x4_any*>(p) = a;
+      *reinterpret_cast<f32x4_any*>(p + 4) = b;
     } else {
-#pragma unroll
-      for (int j = 0; j < 7; ++j)
-        if (col + j < n) p[j] = v[j];
+      if ((n - col) & 4) {
+        *reinterpret_cast<f32x4_any*>(p) = a;
+        a = b;
+        p += 4;
+      }
+      if ((n - col) & 2) {
+        *reinterpret_cast<f32x2_any*>(p) = f32x2{a[0], a[1]};
+        a[0] = a[2];
+        p += 2;
+      }
+      if ((n - col) & 1) *p = a[0];
     }
   }
 }
