@@ -766,7 +766,7 @@ static qlora_status run_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s,
   if (!x || !g || !codes || !absmax8 || !c2 || !A || !B || !grad_A || !grad_B) return QLORA_ERR_NULL;
   if (ckpt && (!x_scales || !u)) return QLORA_ERR_NULL;
   // the checkpointed product addresses v's planes with 32-bit offsets
-  if (ckpt && token_planes_bytes(M, r) >= ((size_t)1 << 32)) return QLORA_ERR_SHAPE;
+  if (ckpt && token_planes_bytes(M, r) >= ((size_t)1 << 31)) return QLORA_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(g) || !aligned16(codes) || !aligned16(absmax8) || !aligned16(c2) ||
       !aligned16(A) || !aligned16(B) || !aligned16(grad_A) || !aligned16(grad_B) || (u && !aligned16(u)) ||
       (grad_x && !aligned16(grad_x)) || (ckpt && !aligned16(x_scales)))

@@ -1106,8 +1106,8 @@ __global__ __launch_bounds__(64 * ck::WAVES) void skinny_token_ckpt_kernel(const
   const brsrc_t rs = make_rsrc(scales, sbytes);
   const brsrc_t rp = make_rsrc(P, pbytes);
   // Offsets of stage 0; a lane that has nothing to load starts past the end
-  // of its tensor (and stays there: tensors are shorter than 2^30 bytes and a
-  // split's offsets grow by less than that).
+  // of its tensor (and stays there: the tensors are shorter than 2^31 bytes and
+  // a split's offsets grow by less than that).
   int xrow[XPW];
   uint32_t xo[XPW], po[PPW];
 #pragma unroll

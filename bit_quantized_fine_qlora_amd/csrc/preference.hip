@@ -100,14 +100,14 @@ __global__ __launch_bounds__(256) void pref_rows_kernel(PrefRowArgs a) {
     const int64_t t = item / a.splits;
     const int sp = (int)(item - t * a.splits);
     const int64_t label = a.labels[t];
-    if (sp == 0 && tid == 0 && a.coef) a.coef[t] = 0.0f;
-    if (!scored(label)) {
-      if (sp == 0 && tid == 0) {
+    if (sp == 0 && tid == 0) {
+      if (a.coef) a.coef[t] = 0.0f;
+      if (a.splits > 1 || !scored(label)) {  // a row of chunks is finished with its sequence
         a.lse[t] = 0.0f;
         a.lp[t] = 0.0f;
       }
-      continue;
     }
+    if (!scored(label)) continue;
     const int v0 = sp * a.chunk;
     const int v1 = v0 + a.chunk < a.V ? v0 + a.chunk : a.V;
     MaxSum r{-INFINITY, 0.0f};

@@ -85,9 +85,15 @@ __device__ __forceinline__ Raw8<XT> load_full8(const RowSrc& s, int64_t row, int
 // place and clears what the row does not have.
 template <int XT>
 __device__ __forceinline__ Raw8<XT> load_piece8(const RowSrc& s, int64_t row, int n, int col) {
-  Raw8<XT> r = load_full8<XT>(RowSrc{s.p, s.scales}, row, n, col + 8 <= n ? col : col < n ? n - 8 : 0);
-  if constexpr (XT == kCkpt8) r.c = s.scales[row * ckpt_pitch(n) + (col < n ? col >> 5 : 0)];
-  return r;
+  const int from = col + 8 <= n ? col : col < n ? n - 8 : 0;
+  if constexpr (XT == kCkpt8) {
+    Raw8<XT> r;
+    r.k = *reinterpret_cast<const u32x2_any*>(static_cast<const uint8_t*>(s.p) + row * n + from);
+    r.c = s.scales[row * ckpt_pitch(n) + (col < n ? col >> 5 : 0)];
+    return r;
+  } else {
+    return load_full8<XT>(s, row, n, from);
+  }
 }
 
 template <int XT>

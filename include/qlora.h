@@ -430,6 +430,7 @@ qlora_status qlora_checkpoint_unpack(int64_t M, int64_t n, const int8_t* codes, 
  * (x_codes, x_scales as above, of the M x n input): x enters one product,
  * grad_A = bf16(s v^T x), which restores it on chip.  u must be given (the
  * forward's u_out; x is not exact enough to recompute it, and u is small).
+ * Also requires M r < 2^29 (32-bit offsets).
  * Everything else, the workspace (op QLORA_OP_BWD, or QLORA_OP_BWD_DROPOUT
  * when p > 0) and qlora_linear_check included, as for qlora_linear_bwd_ex.
  */
@@ -507,7 +508,8 @@ qlora_status qlora_norm_bwd(int32_t kind, int32_t x_type, int32_t w_type, int64_
  *            offsets[s] .. offsets[s + 1] - 1 (none: its sum is 0).  Tokens
  *            outside every sequence count as unscored.  Values outside
  *            0 .. T are held within it.
- *   lse      device out, T fp32: log sum exp of each scored row.
+ *   lse      device out, T fp32: log sum exp of each scored row, 0 for tokens
+ *            that are out (unspecified for scored ones outside every sequence).
  *   logps    device out, one fp32 per sequence: the sum over its scored
  *            tokens of logits[t][labels[t]] - lse[t].
  * Rows are reduced in fp32 with a running maximum, sums over tokens in 64
