@@ -1047,15 +1047,19 @@ __global__ __launch_bounds__(256) void skinny_token_kernel(const uint16_t* __res
 // exact, so the MFMA operands are the bits that restoring X to memory would
 // give.  16-byte unit u of token row t sits at slot u ^ (t % 16): the 8 rows
 // of a transposed read and the 1 KB block writes are free of bank conflicts.
-// 8192 x 28672, 64 ranks: 76 us (the same product of the bf16 tensor 105 us,
-// restoring through registers before LDS 263 us).  Its loads alone, with
-// nothing computed, take 66 us: X alone 45 us (the card streams it in 41 us
-// at any tile shape and ring depth), the planes' second stream through the
-// same load path 14 us and the scale words, 4 bytes of a line each, 9 us.
-// Without the products it takes 69 us, without restoring 66 us.  No faster:
-// 16 waves on 512 columns (75 us, twice the partial sums), restoring a stage
-// ahead (87 us: it needs a stage landed early), waves that take products and
-// restoring in opposite order (95 us), non-temporal loads of X (77 us).
+// 8192 x 28672, 64 ranks: 76 us alone, 78-85 us between other kernels (the
+// same product of the bf16 tensor 105 us, restoring through registers before
+// LDS 263 us).  Its loads alone, with nothing computed, take 66 us: X alone 45
+// us (the card streams it in 41 us at any tile shape and ring depth), the
+// planes' second stream through the same load path 14 us and the scale words,
+// 4 bytes of a line each, 9 us.  Its LDS reads, restoring and products alone,
+// with nothing loaded, take 71 us, of which the products are 5 us and restoring
+// 12 us: the rest is a chain of barrier, LDS latency and restoring in each of
+// its stages that two waves a SIMD do not hide.  No faster: 16 waves on 512
+// columns or two workgroups a CU (74-75 us, twice the partial sums), a stage of
+// 128 tokens (94 us), restoring a stage ahead (87 us), waves that take products
+// and restoring in opposite order (95 us), scales made a stage ahead in LDS (a
+// third fewer vector operations, 76 us), non-temporal loads of X (77 us).
 namespace ck {
 constexpr int WAVES = 8;
 constexpr int TJ = 32 * WAVES;  // columns per workgroup

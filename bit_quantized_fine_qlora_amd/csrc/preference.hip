@@ -11,10 +11,12 @@
 // with a running maximum, and once, element by element, for the gradient.
 // Rows whose label is negative are neither read nor scored; their gradient is
 // written as zeros.  Both passes are bound by HBM.  8 pairs, 6144 x 131072
-// bf16 logits, 60 % of the tokens scored: rows 172 us (966 MB, 5.6 TB/s),
-// sequences 9 us, gradient 453 us (2.58 GB, 5.7 TB/s; a plain copy moves
-// 5.1-5.3).  The logits' loads carry the non-temporal hint: 188 us and 486 us
-// without.  5 pairs, 1501 x 50021 fp32: 48 us (180 MB) and 74 us (480 MB).
+// bf16 logits, 60 % of the tokens scored: rows 154-172 us (966 MB, 5.6-6.3
+// TB/s), sequences 8 us, gradient 436-453 us (2.58 GB, 5.7-5.9 TB/s; a plain
+// copy moves 5.0-5.3).  The logits' loads carry the non-temporal hint: 188 us
+// and 486 us without, on the card of the slower figures.  5 pairs, 1501 x 50021
+// fp32: 48-58 us (180 MB) and 74-81 us (480 MB), the slower between other
+// kernels.
 #include <algorithm>
 
 #include "rows.h"
