@@ -11,9 +11,13 @@ constexpr int64_t kNormMaxWidth = 16384;
 // thread t is at column 8 (t + 64 NW i); 512 NW VPT >= n.  One wave a row as
 // long as the row fits its registers twice over (no barrier: 65536 x 1000
 // bf16, backward 80 us against 134 us with two waves and a barrier a row);
-// then the fewest waves that leave two pieces a thread, 8 at most (16 waves
-// of one piece for 8192 values: forward 70 us instead of 55 us).
-template <typename F>
+// then the fewest waves that leave two pieces a thread, 8 at most.  Rows of
+// 4097 to 8192 values go by direction: forward 8 waves of two pieces (8192 x
+// 8192 bf16, layer: 55 us, 70 us with 16 waves of one), backward 16 waves of
+// one, whose two gradients' sums and two rows in flight then leave more waves
+// a CU (82 us, 93 us with 8 waves of two; rms from a checkpoint 67 and 73 us;
+// 8192 x 5120 rms 55 and 62 us; 4096 x 8192 fp32 layer 76 and 84 us).
+template <bool kBwd, typename F>
 static void norm_shape(int64_t n, F f) {
   using std::integral_constant;
 #define QLORA_SHAPE(NW_, VPT_) f(integral_constant<int, NW_>{}, integral_constant<int, VPT_>{})
@@ -21,8 +25,9 @@ static void norm_shape(int64_t n, F f) {
   else if (n <= 1024) QLORA_SHAPE(1, 2);
   else if (n <= 2048) QLORA_SHAPE(4, 1);
   else if (n <= 4096) QLORA_SHAPE(8, 1);
-  else if (n <= 8192) QLORA_SHAPE(8, 2);
-  else QLORA_SHAPE(8, 4);
+  else if (n > 8192) QLORA_SHAPE(8, 4);
+  else if constexpr (kBwd) QLORA_SHAPE(16, 1);
+  else QLORA_SHAPE(8, 2);
 #undef QLORA_SHAPE
 }
 

@@ -7,12 +7,11 @@
 // checkpoint, restored in registers.  The weights' gradients add up in
 // registers too: a workgroup walks many rows, a thread always holding the same
 // columns, and writes one fp32 partial row at its end, which a second small
-// kernel adds up in a fixed order (5 us at 512 rows of 8192).  Bound by HBM:
-// 8192 x 8192 bf16 rms 70-84 us (403 MB; it moves by a fifth from card to
-// card), from the 8-bit checkpoint 61-74 us (338 MB), 16384 x 4096 fp32 layer
-// 139 us (805 MB, 5.8 TB/s), 2049 x 5001 fp32 layer 36 us (123 MB and 20 MB of
-// partial rows).  The layer norm of 8192 bf16 values takes 93 us: mean, both
-// sums' accumulators and two rows in flight leave room for one workgroup a CU.
+// kernel adds up in a fixed order (5 us at 256 rows of 8192).  Bound by HBM:
+// 8192 x 8192 bf16 rms 75-78 us (403 MB), layer 81-84 us, rms from the 8-bit
+// checkpoint 66-68 us (338 MB), 16384 x 4096 fp32 layer 139 us (805 MB, 5.8
+// TB/s), 2049 x 5001 fp32 layer 34-36 us (123 MB and 20 MB of partial rows);
+// without the weights' gradients 70, 73, 61, 129 and 28 us.
 #include "norm.h"
 
 namespace qlora {
@@ -223,16 +222,17 @@ int64_t norm_max_width() { return kNormMaxWidth; }
 // Workgroups of the backward pass, each one partial row of each gradient.
 // More of them hide more of a row's latency and cost a partial row each,
 // written and read in fp32, as much as about two rows of x, g and grad_x: two
-// a CU for 8-wave rows once each has 16 rows (4096 x 4096 bf16: 26 us, 37 us
-// with one a CU; 2049 x 5001 fp32: 41 us, 36 us with one a CU), eight a CU
+// a CU for rows of 4096 values once each has 16 rows (4096 x 4096 bf16: 26 us,
+// 37 us with one a CU), one a CU for longer ones (2049 x 5001 fp32: 36 us, 41
+// us with two; 8192 x 8192 bf16 rms 75 and 78 us), eight a CU
 // where a wave takes a row of two pieces (65536 x 1000: 80 us, 95 us with
 // four).
 static int64_t norm_bwd_groups(int64_t M, int64_t n) {
   int64_t groups = 0;
-  norm_shape(n, [&](auto nw, auto vpt) {
+  norm_shape<true>(n, [&](auto nw, auto vpt) {
     constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
     const int64_t want = (M + norm_rows(NW) - 1) / norm_rows(NW), cus = device_cus();
-    const int64_t per_cu = NW == 1 ? 4 * VPT : NW == 4 ? 4 : VPT == 4 || M < 16 * cus ? 1 : 2;
+    const int64_t per_cu = NW == 1 ? 4 * VPT : NW == 4 ? 4 : n > 4096 || M < 16 * cus ? 1 : 2;
     groups = want < per_cu * cus ? want : per_cu * cus;
   });
   return groups;
@@ -249,7 +249,7 @@ size_t norm_bwd_ws_bytes(int layer, int64_t M, int64_t n, int accs) {
 
 template <bool kLayer, bool kAcc, int XT, int WT>
 static void norm_bwd_shaped(const NormBwdArgs& a, hipStream_t stream) {
-  norm_shape(a.n, [&](auto nw, auto vpt) {
+  norm_shape<true>(a.n, [&](auto nw, auto vpt) {
     constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
     hipLaunchKernelGGL((norm_bwd_kernel<kLayer, kAcc, XT, WT, NW, VPT>), dim3((unsigned)norm_bwd_groups(a.M, a.n)),
                        dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);

@@ -127,7 +127,7 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
 
 template <bool kLayer, int XT, int WT>
 static void norm_fwd_typed(const NormFwdArgs& a, hipStream_t stream) {
-  norm_shape(a.n, [&](auto nw, auto vpt) {
+  norm_shape<false>(a.n, [&](auto nw, auto vpt) {
     constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
     const int64_t wgs = (a.M + norm_rows(NW) - 1) / norm_rows(NW);
     const int64_t most = (int64_t)device_cus() * (NW == 1 ? 16 : NW == 4 ? 8 : 4);
