@@ -1,6 +1,5 @@
 // C ABI of the QLoRA adapted-linear library: argument checks, workspace
 // layout, kernel dispatch and optional kernel timing.  Declared in qlora.h.
-#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -69,7 +68,7 @@ void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, 
 void launch_token_grad_ckpt(const uint8_t* codes, const uint8_t* scales, int64_t M, int64_t J, const float* Y, int R,
                             int splits, float* part, hipStream_t stream, const DropoutDev& drop,
                             const uint16_t* planes);
-int token_grad_ckpt_splits(int64_t M, int64_t J, int R);
+int token_grad_ckpt_splits(int64_t M, int64_t J, int R, int64_t room);
 size_t token_planes_bytes(int64_t M, int R);
 void launch_factor_planes(const float* Y, int nsplit, int64_t M, int R, uint16_t* P, float* Yout, const float* Y2,
                           uint16_t* P2, hipStream_t stream);
@@ -325,7 +324,7 @@ FwdWs fwd_ws(int64_t M, int64_t n, int64_t m, int32_t r) {
 }
 
 struct BwdWs {
-  size_t Bt, part_uv, u, v, gA, gB, gpad, vpart, gbpart, dterm, planes, uplanes, ksplit, total;
+  size_t Bt, part_uv, u, v, gA, gA_ckpt, gB, gpad, vpart, gbpart, dterm, planes, uplanes, ksplit, total;
   int su, sv, sa, sb;
   int sc;         // token splits of grad_A from a checkpointed input
   bool gpass;     // v and grad_B from one read of g
@@ -344,18 +343,24 @@ BwdWs bwd_ws(int64_t M, int64_t n, int64_t m, int32_t r, bool dropout = false) {
   w.su = down_proj_splits(M, n, r);
   w.sv = down_proj_splits(M, w.m_pad, r);
   w.sa = token_grad_splits(M, n, r);
-  w.sc = token_grad_ckpt_splits(M, n, r);
   w.sb = token_grad_splits(M, w.m_pad, r);
   w.gpass = gpass_supported(r);
   // B^T for v = g B, except where the stream reads B itself
   w.Bt = (w.gpass || down_proj_bt_supported(r)) ? 0 : L.take((size_t)w.m_pad * r * 2);
+  w.v = L.take((size_t)M * r * sizeof(float));
+  // From part_uv to the end of vpart (of gA without the g pass) nothing is in
+  // use once v and its planes are made, if the caller gave u: the split sums
+  // of grad_A from a checkpointed input go over all of it, so that their
+  // larger number does not make the workspace larger.  Where they are more
+  // than it holds (few tokens on a wide layer) the splits are what fits.
   const int suv = w.gpass ? w.su : (w.su > w.sv ? w.su : w.sv);
   w.part_uv = L.take((size_t)suv * M * r * sizeof(float));
   w.u = L.take((size_t)M * r * sizeof(float));
-  w.v = L.take((size_t)M * r * sizeof(float));
-  w.gA = L.take((size_t)std::max(w.sa, w.sc) * n * r * sizeof(float));
-  w.gB = w.gpass ? 0 : L.take((size_t)w.sb * w.m_pad * r * sizeof(float));
+  w.gA = L.take((size_t)w.sa * n * r * sizeof(float));
   w.vpart = w.gpass ? L.take((size_t)gpass_splits_f(M, w.m_pad, r) * M * r * sizeof(float)) : 0;
+  w.gA_ckpt = w.part_uv;
+  w.sc = token_grad_ckpt_splits(M, n, r, (int64_t)((L.total - w.gA_ckpt) / ((size_t)n * r * sizeof(float))));
+  w.gB = w.gpass ? 0 : L.take((size_t)w.sb * w.m_pad * r * sizeof(float));
   w.gbpart = w.gpass ? L.take((size_t)gpass_splits_t(M) * w.m_pad * r * sizeof(float)) : 0;
   // dropout: the masked adapter part of grad_x in fp32
   w.dterm = dropout ? L.take((size_t)M * n * sizeof(float)) : 0;
@@ -828,19 +833,18 @@ static qlora_status run_bwd(int64_t M, int64_t n, int64_t m, int32_t r, float s,
     // sums of grad_B and grad_A in one launch, which also clears the grad_x
     // GEMM's hand-off words
     const int sa = ckpt && !drop ? w.sc : w.sa;
+    float* const gA = at<float>(workspace, ckpt && !drop ? w.gA_ckpt : w.gA);
     if (ckpt)
-      launch_token_grad_ckpt(static_cast<const uint8_t*>(x), x_scales, M, n, v, r, sa, at<float>(workspace, w.gA),
-                             hs, dd, vplanes);
+      launch_token_grad_ckpt(static_cast<const uint8_t*>(x), x_scales, M, n, v, r, sa, gA, hs, dd, vplanes);
     else
-      launch_token_grad(static_cast<const uint16_t*>(x), M, n, v, r, w.sa, at<float>(workspace, w.gA), hs, &dd,
-                        vplanes, true);
+      launch_token_grad(static_cast<const uint16_t*>(x), M, n, v, r, sa, gA, hs, &dd, vplanes, true);
     const SyncZero z = gemm_split_sync(M, n, w.m_pad, ksplit);
     if (w.gpass)
       launch_reduce_grads(at<float>(workspace, w.gbpart), gpass_splits_t(M), mk, m, s, grad_B,
-                          at<float>(workspace, w.gA), sa, n, n, s * inv_keep, grad_A, r, hs, z);
+                          gA, sa, n, n, s * inv_keep, grad_A, r, hs, z);
     else
-      launch_reduce_grads(at<float>(workspace, w.gB), w.sb, mk, m, s, grad_B, at<float>(workspace, w.gA), sa, n, n,
-                          s * inv_keep, grad_A, r, hs, z);
+      launch_reduce_grads(at<float>(workspace, w.gB), w.sb, mk, m, s, grad_B, gA, sa, n, n, s * inv_keep, grad_A, r,
+                          hs, z);
   }
   if (grad_x) {
     if (drop) {

@@ -1462,15 +1462,17 @@ void launch_token_grad(const uint16_t* X, int64_t M, int64_t J, const float* Y, 
 }
 
 // Token splits of the reduction over a checkpointed X: as token_grad_splits,
-// for workgroups of 256 columns.
+// for workgroups of 256 columns and splits of at least 256 tokens; at most
+// `room`, the partials that the caller has memory for.
 static int ckpt_wgs_per_cu(int R) { return rank_blocks(R) <= 2 ? 2 : 1; }
-int token_grad_ckpt_splits(int64_t M, int64_t J, int R) {
+int token_grad_ckpt_splits(int64_t M, int64_t J, int R, int64_t room) {
   const int64_t tiles = cdiv(J, ck::TJ);
   const int64_t slots = (int64_t)ckpt_wgs_per_cu(R) * device_cus();
   int64_t want = cdiv(slots, tiles);
   const int64_t most = cdiv(M, 256);
   if (want > most) want = most;
   if (want > 64) want = 64;
+  if (want > room) want = room;
   if (want < 1) want = 1;
   want = fewest_rounds_splits(tiles, slots, want);
   return (int)cdiv(M, cdiv(cdiv(M, want), ck::TS) * ck::TS);
