@@ -249,7 +249,8 @@ __global__ __launch_bounds__(64 * kSeqWaves) void pref_seq_kernel(PrefSeqArgs a)
       const float up = z >= 0.0f ? near : far, down = z >= 0.0f ? far : near;  // sigma(z), sigma(-z)
       const float su = l + __builtin_fmaxf(-z, 0.0f), sd = l + __builtin_fmaxf(z, 0.0f);  // their -log
       const float c = a.beta * a.inv_pairs * (e * up - (1.0f - e) * down);
-      only = (1.0f - e) * su + (e == 0.0f ? 0.0f : e * sd);
+      // an infinite margin makes one of the logarithms infinite: where its factor is 0 it does not count
+      only = (e == 1.0f ? 0.0f : (1.0f - e) * su) + (e == 0.0f ? 0.0f : e * sd);
       if (tid == 0) a.pair_loss[i] = only;
 #pragma unroll
       for (int k = 0; k < 2; ++k)

@@ -527,7 +527,9 @@ qlora_status qlora_sequence_logps(int32_t type, int64_t T, int64_t V, int64_t se
  *   loss = mean over pairs of -(1 - e) log sigma(z_i) - e log sigma(-z_i)
  *   ref_logps  device, 2 pairs fp32: the reference model's log-probabilities
  *            (qlora_sequence_logps on its logits), or NULL for zeros.
- *   beta finite; label_smoothing e in [0, 1].
+ *   beta finite; label_smoothing e in [0, 1]: where a factor, e or 1 - e, is
+ *            0, its term is 0, also for an infinite z (a label whose logit is
+ *            -infinity).
  *   loss     device out, 1 fp32.      logps, lse: as above.
  *   coef     device out, T fp32: dloss / dlog-probability of each token (0
  *            for unscored ones), which the backward reads.
