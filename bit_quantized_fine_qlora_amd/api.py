@@ -236,11 +236,20 @@ def merge_adapter(q: QuantizedWeight, A: torch.Tensor, B: torch.Tensor, s: float
     return out
 
 
+def _room(need: int, device, workspace):
+    """A workspace of `need` bytes: the given one where it is large enough, or a new one."""
+    if workspace is not None:
+        if workspace.device != device:
+            raise ValueError(f"workspace: must be on {device}, got one on {workspace.device}")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: must be contiguous")
+        if workspace.numel() >= need:
+            return workspace
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+
+
 def _workspace(op, M, n, m, r, device, workspace):
-    need = workspace_bytes(op, M, n, m, r)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    return workspace
+    return _room(workspace_bytes(op, M, n, m, r), device, workspace)
 
 
 def _dropout(dropout):
@@ -384,6 +393,10 @@ def linear_bwd(x: torch.Tensor, g: torch.Tensor, q: QuantizedWeight, A: torch.Te
         gB = torch.empty((m, r), dtype=torch.bfloat16, device=x.device)
     else:
         gx, gA, gB = out
+        if gx is not None:
+            _need(gx, torch.bfloat16, (M, n), "out[0]")
+        _need(gA, torch.bfloat16, (r, n), "out[1]")
+        _need(gB, torch.bfloat16, (m, r), "out[2]")
     if ckpt:
         op = QLORA_OP_BWD if dropout is None else QLORA_OP_BWD_DROPOUT
         ws = _workspace(op, M, n, m, r, x.device, workspace)
@@ -521,8 +534,7 @@ def norm_bwd(x, g: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, mean: torc
     lib = _lib.load()
     kind = NORM_RMS if mean is None else NORM_LAYER
     need = int(lib.qlora_norm_workspace_bytes(kind, M, n, 2 if gb is not None else 1 if gw is not None else 0))
-    if need and (workspace is None or workspace.numel() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=g.device)
+    workspace = _room(need, g.device, workspace) if need else None
     st = lib.qlora_norm_bwd(kind, xt, wt, M, n, xp, xs, _ptr(g), _ptr(w),
                             _ptr(mean), _ptr(rstd), _ptr(out), _ptr(gw), _ptr(gb), _ptr(workspace),
                             workspace.numel() if workspace is not None else 0, _stream(g.device))
@@ -551,10 +563,7 @@ def _packed(logits, labels, offsets):
 
 
 def _preference_workspace(T, V, pairs, device, workspace):
-    need = int(_lib.load().qlora_preference_workspace_bytes(T, V, pairs))
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
-    return workspace
+    return _room(int(_lib.load().qlora_preference_workspace_bytes(T, V, pairs)), device, workspace)
 
 
 def sequence_logps(logits: torch.Tensor, labels: torch.Tensor, offsets: torch.Tensor,
