@@ -505,14 +505,22 @@ def norm_fwd(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor | None = None, ki
 
 def norm_bwd(x, g: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, mean: torch.Tensor | None = None,
              bias: bool = False, need_grad_w: bool = True, out: torch.Tensor | None = None,
-             workspace: torch.Tensor | None = None):
+             workspace: torch.Tensor | None = None, kind: int | None = None):
     """Backward of norm_fwd: (grad_x like g, grad_w, grad_b like w).
 
     x: the forward's input or its Checkpoint8 (g is bf16 then).  mean: the
-    forward's, None for NORM_RMS.  grad_b is None without bias, both weights'
+    forward's, None for NORM_RMS.  kind: the forward's; a mean that does not
+    go with it, missing or too many, is refused.  Without kind a mean means
+    NORM_LAYER and none NORM_RMS.  grad_b is None without bias, both weights'
     gradients without need_grad_w.
     """
     M, n = x.shape
+    if kind is None:
+        kind = NORM_RMS if mean is None else NORM_LAYER
+    elif kind == NORM_LAYER and mean is None:
+        raise ValueError("mean: required with NORM_LAYER")
+    elif kind == NORM_RMS and mean is not None:
+        raise ValueError("mean: NORM_RMS has none")
     if isinstance(x, Checkpoint8):
         x.check("x")
         xt, xp, xs, gtype = _CKPT8, _ptr(x.codes), _ptr(x.scales), torch.bfloat16
@@ -532,10 +540,9 @@ def norm_bwd(x, g: torch.Tensor, w: torch.Tensor, rstd: torch.Tensor, mean: torc
     gw = torch.empty_like(w) if need_grad_w else None
     gb = torch.empty_like(w) if need_grad_w and bias else None
     lib = _lib.load()
-    kind = NORM_RMS if mean is None else NORM_LAYER
-    need = int(lib.qlora_norm_workspace_bytes(kind, M, n, 2 if gb is not None else 1 if gw is not None else 0))
+    need = int(lib.qlora_norm_workspace_bytes(int(kind), M, n, 2 if gb is not None else 1 if gw is not None else 0))
     workspace = _room(need, g.device, workspace) if need else None
-    st = lib.qlora_norm_bwd(kind, xt, wt, M, n, xp, xs, _ptr(g), _ptr(w),
+    st = lib.qlora_norm_bwd(int(kind), xt, wt, M, n, xp, xs, _ptr(g), _ptr(w),
                             _ptr(mean), _ptr(rstd), _ptr(out), _ptr(gw), _ptr(gb), _ptr(workspace),
                             workspace.numel() if workspace is not None else 0, _stream(g.device))
     _lib.check(st, "qlora_norm_bwd")

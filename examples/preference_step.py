@@ -86,9 +86,9 @@ def backward(model, kept, grad_logits):
     """(weights, gradient) pairs."""
     inner, head = model["inner"], model["head"]
     gz, gA2, gB2 = Q.linear_bwd(kept["z"], grad_logits, head["q"], head["A"].copy, head["B"].copy, SCALE, u=kept["u2"])
-    gx1, gw2, _ = Q.norm_bwd(kept["x1"], gz, model["norm2"].copy, kept["rstd2"])
+    gx1, gw2, _ = Q.norm_bwd(kept["x1"], gz, model["norm2"].copy, kept["rstd2"], kind=Q.NORM_RMS)
     gy, gA1, gB1 = Q.linear_bwd(kept["y"], gx1, inner["q"], inner["A"].copy, inner["B"].copy, SCALE, u=kept["u1"])
-    _, gw1, _ = Q.norm_bwd(kept["x0"], gy, model["norm1"].copy, kept["rstd1"])
+    _, gw1, _ = Q.norm_bwd(kept["x0"], gy, model["norm1"].copy, kept["rstd1"], kind=Q.NORM_RMS)
     return [(inner["A"], gA1), (inner["B"], gB1), (head["A"], gA2), (head["B"], gB2), (model["norm1"], gw1),
             (model["norm2"], gw2)]
 
