@@ -64,9 +64,16 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# torch's own short way to a device's current stream, 0.1 us where the stream
+# object takes 1.9; not part of its documented interface, so not relied on.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device=None):
+    if _raw_stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
     index = device.index if device is not None else None
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
+    return _raw_stream(torch.cuda.current_device() if index is None else index)
 
 
 def _need(t: torch.Tensor, dtype, shape, name: str):
