@@ -57,6 +57,34 @@ __device__ __forceinline__ void finish_row(int n, int t, int threads, Raw8<XT> (
   }
 }
 
+// Sum of a value over the NW waves that share a row, the waves' sums added in
+// 64 bits; every wave gets it.  Slots are taken in turn, as in row_sums below.
+template <int NW>
+__device__ __forceinline__ double row_sum64(float v, float (&red)[2][NW], int& turn, int wave) {
+  v = wave_sum(v);
+  if constexpr (NW == 1) {
+    return (double)v;
+  } else {
+    auto& slot = red[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 63) == 0) slot[wave] = v;
+    __syncthreads();
+    double s = (double)slot[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) s += (double)slot[i];
+    return s;
+  }
+}
+
+// v^(-1/2): the hardware's 64-bit estimate, good to about 2^-23, and one Newton
+// step, r + r (1 - v r^2) / 2; at 0 and infinity, where the step has no value,
+// the estimate itself.
+__device__ __forceinline__ float inverse_root(double v) {
+  const double r = __builtin_amdgcn_rsq(v);
+  const double e = __builtin_fma(-v * r, r, 1.0);
+  return (float)(e == e ? __builtin_fma(0.5 * r, e, r) : r);
+}
+
 // Sums of K values over the NW waves that share a row; every wave gets them.
 // Calls take the two slots of `red` in turn: a wave writes a slot again only
 // after the barrier of the call between, which no wave reaches before it has

@@ -4,7 +4,10 @@
 //   y = (x - mean) rstd w + b
 // A row stays in registers between its uses, so x is read from memory once;
 // the variance is the mean of squared differences (a second pass over the
-// registers), not a difference of means.  With a checkpoint asked for, y is
+// registers), not a difference of means.  From a wave's sum on the statistics
+// are in 64 bits and each of them is rounded to fp32 once: in fp32 throughout,
+// rstd's error was half as large again (0.75 against 0.49 units of 2^-24 in
+// the mean square, 0.45 being the last rounding's) at the same time.  With a checkpoint asked for, y is
 // also written in 8 bits while it is in registers, which saves the packing
 // kernel's read.  Bound by HBM: 8192 x 8192 bf16, rms 45-47 us (268 MB, 5.7-5.9
 // TB/s; a plain copy moves 5.1-5.3), with the checkpoint 55-58 us (338 MB),
@@ -16,7 +19,8 @@ namespace qlora {
 struct NormFwdArgs {
   int n;
   int64_t M;
-  float eps, inv_n;
+  float eps;
+  double inv_n;
   const void* x;
   const void* w;
   const void* b;  // may be null
@@ -32,7 +36,7 @@ struct NormFwdArgs {
 template <bool kLayer, int XT, int WT, int NW, int VPT>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormFwdArgs a) {
 #pragma clang fp contract(off)  // the same roundings in every instantiation
-  __shared__ float red[2][1][NW];
+  __shared__ float red[2][NW];
   int turn = 0;
   constexpr int TPR = 64 * NW;
   const int wave = (int)threadIdx.x >> 6;
@@ -55,18 +59,17 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
     load_row<XT, VPT>(src, row + step < a.M ? row + step : row, a.n, t, TPR, next);
     float mean = 0.0f;
     if constexpr (kLayer) {
-      float s[1] = {0.0f};
+      float s = 0.0f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         float v[8];
         raw_to_f32<XT>(r[i], v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += v[j];
+        for (int j = 0; j < 8; ++j) s += v[j];
       }
-      row_sums<NW, 1>(s, red, turn, wave);
-      mean = s[0] * a.inv_n;
+      mean = (float)(row_sum64<NW>(s, red, turn, wave) * a.inv_n);
     }
-    float s[1] = {0.0f};
+    float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int col = 8 * (t + TPR * i);
@@ -79,10 +82,9 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
         if constexpr (kLayer) d = col + j < a.n ? d - mean : 0.0f;
         q = __builtin_fmaf(d, d, q);
       }
-      s[0] += q;
+      s += q;
     }
-    row_sums<NW, 1>(s, red, turn, wave);
-    const float rstd = 1.0f / __builtin_sqrtf(s[0] * a.inv_n + a.eps);
+    const float rstd = inverse_root(row_sum64<NW>(s, red, turn, wave) * a.inv_n + (double)a.eps);
     if (t == 0) {
       a.rstd[row] = rstd;
       if constexpr (kLayer) a.mean[row] = mean;
@@ -139,7 +141,7 @@ static void norm_fwd_typed(const NormFwdArgs& a, hipStream_t stream) {
 void launch_norm_fwd(int layer, int x_type, int w_f32, int64_t M, int64_t n, float eps, const void* x, const void* w,
                      const void* b, void* y, float* mean, float* rstd, int8_t* codes, uint8_t* scales,
                      hipStream_t stream) {
-  const NormFwdArgs a{(int)n, M, eps, 1.0f / (float)n, x, w, b, y, mean, rstd, codes, scales};
+  const NormFwdArgs a{(int)n, M, eps, 1.0 / (double)n, x, w, b, y, mean, rstd, codes, scales};
   if (x_type == kF32) layer ? norm_fwd_typed<true, kF32, kF32>(a, stream) : norm_fwd_typed<false, kF32, kF32>(a, stream);
   else if (w_f32) layer ? norm_fwd_typed<true, kBf16, kF32>(a, stream) : norm_fwd_typed<false, kBf16, kF32>(a, stream);
   else layer ? norm_fwd_typed<true, kBf16, kBf16>(a, stream) : norm_fwd_typed<false, kBf16, kBf16>(a, stream);
