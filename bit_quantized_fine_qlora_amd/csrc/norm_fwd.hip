@@ -32,8 +32,10 @@ struct NormFwdArgs {
 };
 
 // Persistent workgroups walk the rows; the next row's loads go out before
-// the current row is reduced.
-template <bool kLayer, int XT, int WT, int NW, int VPT>
+// the current row is reduced.  kKeepBias: the bias stays in registers.  Loaded
+// in each row it is waited for after the next row's loads, which go out before
+// it, and makes every row wait for those.
+template <bool kLayer, bool kKeepBias, int XT, int WT, int NW, int VPT>
 __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormFwdArgs a) {
 #pragma clang fp contract(off)  // the same roundings in every instantiation
   __shared__ float red[2][NW];
@@ -45,9 +47,13 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
   const RowSrc src{a.x, nullptr};
   int64_t row = (int64_t)blockIdx.x * norm_rows(NW) + (NW == 1 ? wave : 0);
   if (row >= a.M) return;  // a whole workgroup, or (NW = 1, no barriers) a wave
-  Raw8<WT> w[VPT];
+  Raw8<WT> w[VPT], bias[kKeepBias ? VPT : 1];
   load_row<WT, VPT>(RowSrc{a.w, nullptr}, 0, a.n, t, TPR, w);
   finish_row<WT, VPT>(a.n, t, TPR, w);
+  if constexpr (kKeepBias) {
+    load_row<WT, VPT>(RowSrc{a.b, nullptr}, 0, a.n, t, TPR, bias);
+    finish_row<WT, VPT>(a.n, t, TPR, bias);
+  }
   Raw8<XT> next[VPT];
   load_row<XT, VPT>(src, row, a.n, t, TPR, next);
   for (; row < a.M; row += step) {
@@ -97,15 +103,18 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_fwd_kernel(NormF
       raw_to_f32<WT>(w[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = (kLayer ? v[j] - mean : v[j]) * rstd;
-      if (!a.b) {
+      if (!kKeepBias && !a.b) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= wv[j];
       } else {
-        Raw8<WT> b[1];
         float bv[8];
-        load_row<WT, 1>(RowSrc{a.b, nullptr}, 0, a.n, t + TPR * i, 0, b);
-        finish_row<WT, 1>(a.n, t + TPR * i, 0, b);
-        raw_to_f32<WT>(b[0], bv);
+        if constexpr (kKeepBias) {
+          raw_to_f32<WT>(bias[i], bv);
+        } else {
+          load_row<WT, 1>(RowSrc{a.b, nullptr}, 0, a.n, t + TPR * i, 0, bias);
+          finish_row<WT, 1>(a.n, t + TPR * i, 0, bias);
+          raw_to_f32<WT>(bias[0], bv);
+        }
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = __builtin_fmaf(v[j], wv[j], bv[j]);
       }
@@ -133,8 +142,14 @@ static void norm_fwd_typed(const NormFwdArgs& a, hipStream_t stream) {
     constexpr int NW = decltype(nw)::value, VPT = decltype(vpt)::value;
     const int64_t wgs = (a.M + norm_rows(NW) - 1) / norm_rows(NW);
     const int64_t most = (int64_t)device_cus() * (NW == 1 ? 16 : NW == 4 ? 8 : 4);
-    hipLaunchKernelGGL((norm_fwd_kernel<kLayer, XT, WT, NW, VPT>), dim3((unsigned)(wgs < most ? wgs : most)),
-                       dim3(NW == 1 ? 256 : 64 * NW), 0, stream, a);
+    const dim3 grid((unsigned)(wgs < most ? wgs : most)), block(NW == 1 ? 256 : 64 * NW);
+    // A layer norm's bias is kept where the registers are enough (8192 x 8192
+    // bf16 50 us, 57 us loading it in each row; 16384 x 1500 bf16 29 and 36 us).
+    constexpr bool kKeep = kLayer && VPT < 4;
+    if (kKeep && a.b)
+      hipLaunchKernelGGL((norm_fwd_kernel<kLayer, kKeep, XT, WT, NW, VPT>), grid, block, 0, stream, a);
+    else
+      hipLaunchKernelGGL((norm_fwd_kernel<kLayer, false, XT, WT, NW, VPT>), grid, block, 0, stream, a);
   });
 }
 
