@@ -71,14 +71,15 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormB
   int64_t row = (int64_t)blockIdx.x * norm_rows(NW) + (NW == 1 ? wave : 0);
   Raw8<XT> xn[VPT];
   Raw8<GT> gn[VPT];
-  // Where waves share a row, its statistics are loaded ahead of its x and g:
-  // loads are waited for in order, and after the next row's loads they would
-  // make every row wait for all of those before its barrier (8192 x 8192 bf16
-  // rms from a checkpoint 65 us, 69 us so; 8192 x 5120 rms 50 and 56 us; only
-  // fp32 rows of 8192 are 2 to 3 % slower, 154 and 150 us).  A wave that has
-  // its row to itself loads them last: it meets no barrier, and 131072 x 500
-  // rms takes 82 us, 85 us with them first.
-  constexpr bool kStatsFirst = NW > 1;
+  // Where 8 or 16 waves share a row, its statistics are loaded ahead of its x
+  // and g: loads are waited for in order, and after the next row's loads they
+  // would make every row wait for all of those before its barrier (8192 x 8192
+  // bf16 rms from a checkpoint 64 us, 69 us so; 8192 x 5120 rms 50 and 56 us;
+  // 2049 x 5001 fp32 rms 32 and 35; only many long fp32 rows are slower, 8192 x
+  // 8192 rms 152 and 148).  Elsewhere, with more rows in flight a CU, they are
+  // loaded where they are used (131072 x 500 rms 82 us, 85 us with them first;
+  // 32768 x 2048 rms 81 and 84).
+  constexpr bool kStatsFirst = kAhead && NW > 4;
   float mean_n = 0.0f, rstd_n = 0.0f;
   auto load_stats = [&](int64_t at) {
     if constexpr (kLayer) mean_n = a.layer ? a.mean[at] : 0.0f;
@@ -99,7 +100,6 @@ __global__ __launch_bounds__(NW == 1 ? 256 : 64 * NW) void norm_bwd_kernel(NormB
         gr[i] = gn[i];
       }
     } else {
-      if constexpr (kStatsFirst) load_stats(row);
       load_row<XT, VPT>(a.x, row, a.n, t, TPR, xr);
       load_row<GT, VPT>(gsrc, row, a.n, t, TPR, gr);
     }
