@@ -352,7 +352,9 @@ BwdWs bwd_ws(int64_t M, int64_t n, int64_t m, int32_t r, bool dropout = false) {
   // use once v and its planes are made, if the caller gave u: the split sums
   // of grad_A from a checkpointed input go over all of it, so that their
   // larger number does not make the workspace larger.  Where they are more
-  // than it holds (few tokens on a wide layer) the splits are what fits.
+  // than it holds (few tokens on a wide layer) the splits are what fits (300
+  // tokens, 14336 columns, 16 ranks: the adapters' gradients 29 us, 28 us with a
+  // split more; 1150 tokens, 33088 columns, 128 ranks: 76 and 84 us).
   const int suv = w.gpass ? w.su : (w.su > w.sv ? w.su : w.sv);
   w.part_uv = L.take((size_t)suv * M * r * sizeof(float));
   w.u = L.take((size_t)M * r * sizeof(float));

@@ -7,8 +7,8 @@
 // of the backward pass (grad_A).
 //
 // Both kernels move 8 values a lane and are bound by HBM: packing reads 2
-// bytes and writes 33/32 a value, restoring the reverse: 8192 x 8192 36 us each
-// (203 MB, 5.6 TB/s; a plain copy moves 5.1-5.3).  More loads in flight a
+// bytes and writes 33/32 a value, restoring the reverse: 8192 x 8192 36-39 us
+// each (203 MB, 5.2-5.6 TB/s; a plain copy moves 5.0-5.3).  More loads in flight a
 // thread, non-temporal loads and fewer or more workgroups measured 0 to 10 %
 // slower.
 #include "rows.h"

@@ -8,15 +8,22 @@ namespace qlora {
 constexpr int64_t kNormMaxWidth = 16384;
 
 // A row is held by NW waves, VPT pieces of 8 values a thread: piece i of
-// thread t is at column 8 (t + 64 NW i); 512 NW VPT >= n.  One wave a row as
-// long as the row fits its registers twice over (no barrier: 65536 x 1000
-// bf16, backward 80 us against 134 us with two waves and a barrier a row);
-// then the fewest waves that leave two pieces a thread, 8 at most.  Rows of
-// 4097 to 8192 values go by direction: forward 8 waves of two pieces (8192 x
-// 8192 bf16, layer: 55 us, 70 us with 16 waves of one), backward 16 waves of
-// one, whose two gradients' sums and two rows in flight then leave more waves
-// a CU (82 us, 93 us with 8 waves of two; rms from a checkpoint 67 and 73 us;
-// 8192 x 5120 rms 55 and 62 us; 4096 x 8192 fp32 layer 76 and 84 us).
+// thread t is at column 8 (t + 64 NW i); 512 NW VPT >= n.
+//   up to   512 values  1 wave, 1 piece a thread
+//   up to  1024         1 wave, 2 pieces: no barrier (65536 x 1000 bf16 rms
+//                       forward 48 us, 59 us with 2 waves of one and a barrier
+//                       a row; backward 90 and 91 us)
+//   up to  2048         4 waves, 1 piece, and
+//   up to  4096         8 waves, 1 piece: with half the waves and two pieces the
+//                       backward's gradient sums and rows in flight leave too
+//                       few waves a CU (16384 x 1500 bf16 layer 40 us, 51 us
+//                       so; 4096 x 4096 28 and 35 us); the forward alone would
+//                       gain by it (29 and 25 us; 17 and 15 us)
+//   up to  8192         forward 8 waves, 2 pieces (8192 x 8192 bf16 layer 49 us,
+//                       70 us with 16 waves of one), backward 16 waves, 1 piece
+//                       (8192 x 5120 layer 51 us, 53 us with 8 waves of two;
+//                       8192 x 8192 81 and 80 us)
+//   up to 16384         8 waves, 4 pieces
 template <bool kBwd, typename F>
 static void norm_shape(int64_t n, F f) {
   using std::integral_constant;

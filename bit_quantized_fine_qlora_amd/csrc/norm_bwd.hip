@@ -7,11 +7,13 @@
 // checkpoint, restored in registers.  The weights' gradients add up in
 // registers too: a workgroup walks many rows, a thread always holding the same
 // columns, and writes one fp32 partial row at its end, which a second small
-// kernel adds up in a fixed order (5 us at 256 rows of 8192).  Bound by HBM:
-// 8192 x 8192 bf16 rms 75-78 us (403 MB), layer 81-84 us, rms from the 8-bit
-// checkpoint 66-68 us (338 MB), 16384 x 4096 fp32 layer 139 us (805 MB, 5.8
-// TB/s), 2049 x 5001 fp32 layer 34-36 us (123 MB and 20 MB of partial rows);
-// without the weights' gradients 70, 73, 61, 129 and 28 us.
+// kernel adds up in a fixed order (5 us at 256 rows of 8192).  Bound by HBM
+// (operands that no cache holds, both launches): 8192 x 8192 bf16 rms 78 us (403
+// MB, 5.2 TB/s; a plain copy moves 5.0-5.3), layer 81 us, from the 8-bit
+// checkpoint 64 and 67 us (338 MB), 16384 x 4096 fp32 layer 151 us (805 MB, 5.3
+// TB/s); without the weights' gradients 73, 73, 59 (rms) and 146 us.  2049 x 5001
+// fp32 layer, 8 rows a workgroup, is not: 34 us (123 MB and 20 MB of partial
+// rows, 4.2 TB/s), 25 us without the weights' gradients.
 #include "norm.h"
 
 namespace qlora {
@@ -242,11 +244,12 @@ int64_t norm_max_width() { return kNormMaxWidth; }
 // Workgroups of the backward pass, each one partial row of each gradient.
 // More of them hide more of a row's latency and cost a partial row each,
 // written and read in fp32, as much as about two rows of x, g and grad_x: two
-// a CU for rows of 4096 values once each has 16 rows (4096 x 4096 bf16: 26 us,
-// 37 us with one a CU), one a CU for longer ones (2049 x 5001 fp32: 36 us, 41
-// us with two; 8192 x 8192 bf16 rms 75 and 78 us), eight a CU
-// where a wave takes a row of two pieces (65536 x 1000: 80 us, 95 us with
-// four).
+// a CU for rows of 4096 values once each has 16 rows (16384 x 4096 fp32 layer
+// 151 us, 156 us with one a CU; 4096 x 4096 bf16 rms from a checkpoint 23 and
+// 24 us, but from bf16 26 and 24 us), one a CU for longer ones (2049 x 5001
+// fp32 layer 34 us, 39 us with two; 8192 x 8192 bf16 layer 81 and 85 us), eight
+// a CU where a wave takes a row of two pieces (65536 x 1000 bf16 rms 90 us, with
+// four 89; 65536 x 1024 fp32 layer 159 us, with four 149).
 static int64_t norm_bwd_groups(int64_t M, int64_t n) {
   int64_t groups = 0;
   norm_shape<true>(n, [&](auto nw, auto vpt) {

@@ -7,11 +7,13 @@
 // registers), not a difference of means.  From a wave's sum on the statistics
 // are in 64 bits and each of them is rounded to fp32 once: in fp32 throughout,
 // rstd's error was half as large again (0.75 against 0.49 units of 2^-24 in
-// the mean square, 0.45 being the last rounding's) at the same time.  With a checkpoint asked for, y is
-// also written in 8 bits while it is in registers, which saves the packing
-// kernel's read.  Bound by HBM: 8192 x 8192 bf16, rms 45-47 us (268 MB, 5.7-5.9
-// TB/s; a plain copy moves 5.1-5.3), with the checkpoint 55-58 us (338 MB),
-// layer 54 us; rows of odd length, 2049 x 5001 fp32, 25 us (82 MB).
+// the mean square at 8192 values, 0.45 being the last rounding's) at the same
+// time.  With a checkpoint asked for, y is also written in 8 bits while it is
+// in registers, which saves the packing kernel's read.  Bound by HBM (operands
+// that no cache holds): 8192 x 8192 bf16 rms 50 us (268 MB, 5.4 TB/s; a plain
+// copy moves 5.0-5.3), with the checkpoint 65-67 us (338 MB), layer with a bias
+// 49 and 64 us.  2049 x 5001 fp32, two rows a workgroup, is not: rms 22 us,
+// layer 23 us (82 MB, 3.6-3.7 TB/s).
 #include "norm.h"
 
 namespace qlora {

@@ -10,13 +10,16 @@
 // sequences, so the logits are read twice: once for the row sums, in one pass
 // with a running maximum, and once, element by element, for the gradient.
 // Rows whose label is negative are neither read nor scored; their gradient is
-// written as zeros.  Both passes are bound by HBM.  8 pairs, 6144 x 131072
-// bf16 logits, 60 % of the tokens scored: rows 154-172 us (966 MB, 5.6-6.3
-// TB/s), sequences 8 us, gradient 436-453 us (2.58 GB, 5.7-5.9 TB/s; a plain
-// copy moves 5.0-5.3).  The logits' loads carry the non-temporal hint: 188 us
-// and 486 us without, on the card of the slower figures.  5 pairs, 1501 x 50021
-// fp32: 48-58 us (180 MB) and 74-81 us (480 MB), the slower between other
-// kernels.
+// written as zeros.  With thousands of rows both passes are bound by HBM: 8
+// pairs, 6144 x 131072 bf16 logits, 60 % of the tokens scored: rows 154-172 us
+// (966 MB, 5.6-6.3 TB/s), sequences 8 us, gradient 431-453 us (2.58 GB, 5.7-6.0
+// TB/s; a plain copy moves 5.0-5.3).  The logits' loads carry the non-temporal
+// hint: 188 us and 486 us without, on the card of the slower figures.  With
+// fewer the row pass is not, a workgroup to a row and no load in flight while
+// it adds: 5 pairs, 1501 x 50021 fp32, 904 rows scored, 48-60 us (181 MB, 3.0-3.8
+// TB/s), the same with rows of 50048; as many bytes in bf16, 3002 x 50021, 52 us;
+// 6001 x 50021 fp32, 3530 scored, 173 us (706 MB, 4.1 TB/s).  The gradient of the
+// first takes 74-81 us (481 MB, 5.9-6.5 TB/s).
 #include <algorithm>
 
 #include "rows.h"
@@ -68,7 +71,7 @@ struct PrefRowArgs {
   uint32_t* ticket;  // cleared here
 };
 
-// The token's row is out of use (negative label), or its label is none.
+// The token counts: its label is not negative.
 __device__ __forceinline__ bool scored(int64_t label) { return label >= 0; }
 
 template <int XT>
