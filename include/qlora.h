@@ -513,7 +513,10 @@ qlora_status qlora_norm_bwd(int32_t kind, int32_t x_type, int32_t w_type, int64_
  *   logps    device out, one fp32 per sequence: the sum over its scored
  *            tokens of logits[t][labels[t]] - lse[t].
  * Rows are reduced in fp32 with a running maximum, sums over tokens in 64
- * bits, in a fixed order.  Requires T, V >= 1.  Logits of -infinity have
+ * bits, in a fixed order.  lse is one fp32 number: a row's probabilities, and
+ * with them its gradient, are within about 2^-24 |lse| of themselves, so logits
+ * of very large magnitude (a scored row of nothing but the type's lowest value,
+ * say) should be shifted first.  Requires T, V >= 1.  Logits of -infinity have
  * probability 0; a row with NaN, +infinity or no finite value gives NaN.
  */
 size_t qlora_preference_workspace_bytes(int64_t T, int64_t V, int64_t pairs);
