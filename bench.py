@@ -65,14 +65,14 @@ BF16_PEAK_TFLOPS = 2500.0
 # what the same counters read for a plain 1 GiB device copy (FETCH_SIZE x
 # 2.0, WRITE_SIZE x 1.0; see profiles/).  Keyed by "layer/kernel" of the
 # 70B-block step.  Valid only for the GEMM sources they were taken on (the
-# kernel and the header it includes): reported as null once either changes.
+# kernel and the headers it includes): reported as null once either changes.
 # The counters count the L2's requests to the memory fabric, so bytes served
 # by the last-level cache (MALL) are included: an upper bound on HBM bytes.
 # The k and v forwards run every tile as two K halves: their writes are h
 # plus one fp32 half-sum per tile.
-GEMM_SRC = [os.path.join(ROOT, "bit_quantized_fine_qlora_amd", "csrc", f) for f in ("gemm_linear.hip", "qlora_common.h")]
+GEMM_SRC = [os.path.join(ROOT, "bit_quantized_fine_qlora_amd", "csrc", f) for f in ("gemm_linear.hip", "gemm_tile.h", "qlora_common.h")]
 GEMM_TRAFFIC = {
-    "src_sha1": "283b6faedb84f1f83fab3cd6ceb33c5641383d8a",
+    "src_sha1": "0d15ca5eabaedf931ccc72339e3a821411e72f92",
     "q/fwd_gemm": {"fetch": 1297956352, "write": 134244224},
     "k/fwd_gemm": {"fetch": 584374315, "write": 50344448},
     "v/fwd_gemm": {"fetch": 584374699, "write": 50345301},
