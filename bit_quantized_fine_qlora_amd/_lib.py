@@ -16,6 +16,7 @@ LIB_PATH = os.path.join(_PKG_DIR, "libqlora.so")
 c_i64 = ctypes.c_int64
 c_i32 = ctypes.c_int32
 c_f32 = ctypes.c_float
+c_f64 = ctypes.c_double
 c_vp = ctypes.c_void_p
 c_sz = ctypes.c_size_t
 
@@ -41,6 +42,18 @@ class AdamTensor(ctypes.Structure):
     """qlora_adam_tensor: one adapter tensor of an optimizer step (host struct)."""
     _fields_ = [("count", c_i64), ("param", c_vp), ("param_bf16", c_vp), ("grad", c_vp),
                 ("exp_avg", c_vp), ("exp_avg_sq", c_vp)]
+
+
+class AdamWTensor(ctypes.Structure):
+    """qlora_adamw_tensor: one tensor of an optimizer step over many (host struct)."""
+    _fields_ = [("count", c_i64), ("param", c_vp), ("param_bf16", c_vp), ("grad", c_vp), ("exp_avg", c_vp),
+                ("exp_avg_sq", c_vp), ("exp_avg_steps", c_vp), ("exp_avg_sq_steps", c_vp), ("grad_type", c_i32),
+                ("moments", c_i32)]
+
+
+class AdamWHandle(ctypes.Structure):
+    """qlora_adamw_handle: a plan of steps (host struct)."""
+    _fields_ = [("plan", c_vp), ("tensors", c_i64), ("chunks", c_i64), ("reserved", c_i64)]
 
 
 # name -> (restype, argtypes); mirrors include/qlora.h
@@ -87,6 +100,18 @@ PROTOTYPES = {
     "qlora_preference_fwd": (ctypes.c_int, [c_i32, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_f32, c_f32, c_vp,
                                             c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "qlora_preference_bwd": (ctypes.c_int, [c_i32, c_i64, c_i64, c_vp, c_vp, c_vp, c_vp, c_f32, c_vp, c_vp]),
+    "qlora_experts_workspace_bytes": (c_sz, [ctypes.c_int, c_i64, c_i64, c_i64, c_i64, c_i32]),
+    "qlora_experts_fwd": (ctypes.c_int, [c_i64, c_i64, c_i64, c_i64, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                         c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "qlora_experts_bwd": (ctypes.c_int, [c_i64, c_i64, c_i64, c_i64, c_i32, c_f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                         c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
+    "qlora_adamw_plan_bytes": (c_sz, [ctypes.POINTER(AdamWTensor), c_i64]),
+    "qlora_adamw_plan": (ctypes.c_int, [ctypes.POINTER(AdamWTensor), c_i64, c_vp, c_sz, ctypes.POINTER(AdamWHandle),
+                                        c_vp]),
+    "qlora_grad_clip": (ctypes.c_int, [ctypes.POINTER(AdamWHandle), c_f64, c_vp, c_vp]),
+    "qlora_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWHandle), c_f64, c_f64, c_f64, c_f64, c_f64, c_i64, c_vp,
+                                        c_vp]),
+    "qlora_moment8_values": (ctypes.c_int, [c_i32, c_i64, c_vp, c_vp, c_vp, c_vp]),
     "qlora_linear_check": (ctypes.c_int, [ctypes.c_int, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp]),
     "qlora_profile_enable": (ctypes.c_int, [ctypes.c_int]),
     "qlora_profile_query": (ctypes.c_int, [ctypes.c_char_p, ctypes.POINTER(c_i64), ctypes.POINTER(ctypes.c_double)]),

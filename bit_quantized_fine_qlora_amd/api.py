@@ -644,6 +644,215 @@ def preference_bwd(logits: torch.Tensor, labels: torch.Tensor, saved: Preference
     return out
 
 
+def _experts(x, offsets, q, A, B):
+    """(M, E, n, m, r) of the experts' layer, its operands checked."""
+    M, n = x.shape
+    if A.dim() != 3 or B.dim() != 3:
+        raise ValueError("A, B: expected [experts, r, n] and [experts, m, r], got "
+                         f"{tuple(A.shape)} and {tuple(B.shape)}")
+    E, r, _ = A.shape
+    if E == 0 or q.m % E:
+        raise ValueError(f"q: {q.m} rows are not those of {E} experts")
+    m = q.m // E
+    _need(x, torch.bfloat16, (M, q.n), "x")
+    _need(offsets, torch.int32, (E + 1,), "offsets")
+    _need(A, torch.bfloat16, (E, r, n), "A")
+    _need(B, torch.bfloat16, (E, m, r), "B")
+    return M, E, n, m, r
+
+
+def experts_workspace_bytes(op: int, M: int, E: int, n: int, m: int, r: int) -> int:
+    return int(_lib.load().qlora_experts_workspace_bytes(op, M, E, n, m, r))
+
+
+def experts_fwd(x: torch.Tensor, offsets: torch.Tensor, q: QuantizedWeight, A: torch.Tensor, B: torch.Tensor,
+                s: float, h: torch.Tensor | None = None, u: torch.Tensor | None = None, want_u: bool = True,
+                workspace: torch.Tensor | None = None):
+    """The adapted layer of many experts.  Returns (h bf16 [M, m], u fp32 [M, r] or None).
+
+    x: bf16 [M, n], rows in order of their expert; offsets: int32 [E + 1] on the device, expert e's rows being
+    offsets[e] .. offsets[e + 1] - 1 (none is fine); q: the experts' weights quantized as one [E m, n] weight; A
+    bf16 [E, r, n], B bf16 [E, m, r].  Rows of no expert are not written (where h or u is not given, they hold
+    anything).
+    """
+    M, E, n, m, r = _experts(x, offsets, q, A, B)
+    if h is None:
+        h = torch.empty((M, m), dtype=torch.bfloat16, device=x.device)
+    else:
+        _need(h, torch.bfloat16, (M, m), "h")
+    if u is not None:
+        _need(u, torch.float32, (M, r), "u")
+    elif want_u:
+        u = torch.empty((M, r), dtype=torch.float32, device=x.device)
+    ws = _room(experts_workspace_bytes(QLORA_OP_FWD, M, E, n, m, r), x.device, workspace)
+    st = _lib.load().qlora_experts_fwd(M, E, n, m, r, float(s), _ptr(x), _ptr(offsets), _ptr(q.codes),
+                                       _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(h), _ptr(u), _ptr(ws),
+                                       ws.numel(), _stream(x.device))
+    _lib.check(st, "qlora_experts_fwd")
+    return h, u
+
+
+def experts_bwd(x: torch.Tensor, g: torch.Tensor, offsets: torch.Tensor, q: QuantizedWeight, A: torch.Tensor,
+                B: torch.Tensor, s: float, u: torch.Tensor | None = None, need_grad_x: bool = True, out=None,
+                workspace: torch.Tensor | None = None):
+    """Backward of experts_fwd: (grad_x bf16 [M, n] or None, grad_A bf16 [E, r, n], grad_B bf16 [E, m, r]).
+
+    u: the forward's, or None to recompute it.  out: the three outputs to write (the first None to skip it).
+    grad_x's rows of no expert are not written; an expert without rows gets gradients of zero.
+    """
+    M, E, n, m, r = _experts(x, offsets, q, A, B)
+    _need(g, torch.bfloat16, (M, m), "g")
+    if u is not None:
+        _need(u, torch.float32, (M, r), "u")
+    if out is None:
+        gx = torch.empty((M, n), dtype=torch.bfloat16, device=x.device) if need_grad_x else None
+        gA, gB = torch.empty_like(A), torch.empty_like(B)
+    else:
+        gx, gA, gB = out
+        if gx is not None:
+            _need(gx, torch.bfloat16, (M, n), "out[0]")
+        _need(gA, torch.bfloat16, (E, r, n), "out[1]")
+        _need(gB, torch.bfloat16, (E, m, r), "out[2]")
+    ws = _room(experts_workspace_bytes(QLORA_OP_BWD, M, E, n, m, r), x.device, workspace)
+    st = _lib.load().qlora_experts_bwd(M, E, n, m, r, float(s), _ptr(x), _ptr(g), _ptr(offsets), _ptr(q.codes),
+                                       _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(u), _ptr(gx), _ptr(gA),
+                                       _ptr(gB), _ptr(ws), ws.numel(), _stream(x.device))
+    _lib.check(st, "qlora_experts_bwd")
+    return gx, gA, gB
+
+
+MOMENT_BLOCK = 128
+
+
+@dataclasses.dataclass
+class Moment8:
+    """A moment of AdamWStep in 8 bits: one code an element, one step per 128 of them."""
+    codes: torch.Tensor     # uint8 [count]
+    steps: torch.Tensor     # float32 [ceil(count / 128)]
+    signed: bool            # True for exp_avg, False for exp_avg_sq
+
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.steps.numel()
+
+    def check(self, name: str, count: int) -> None:
+        for t, dtype, shape, part in ((self.codes, torch.uint8, (count,), ".codes"),
+                                      (self.steps, torch.float32, (-(-count // MOMENT_BLOCK),), ".steps")):
+            if t.dtype != dtype:
+                raise TypeError(f"{name}{part}: expected {dtype}, got {t.dtype}")
+            if tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"{name}{part}: expected contiguous {shape}, got {tuple(t.shape)}")
+
+
+def alloc_moment8(count: int, signed: bool, device="cuda", pin_memory: bool = False) -> Moment8:
+    """An 8-bit moment of zeros, on a device or (device "cpu", pin_memory) in pinned host memory."""
+    kw = dict(device=device, pin_memory=pin_memory)
+    return Moment8(torch.zeros(count, dtype=torch.uint8, **kw),
+                   torch.zeros(-(-count // MOMENT_BLOCK), dtype=torch.float32, **kw), signed)
+
+
+def moment8_values(moment: Moment8, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The fp32 values that an 8-bit moment's codes stand for."""
+    n = moment.codes.numel()
+    moment.check("moment", n)
+    _need(moment.codes, torch.uint8, (n,), "moment.codes")
+    if out is None:
+        out = torch.empty(n, dtype=torch.float32, device=moment.codes.device)
+    else:
+        _need(out, torch.float32, (n,), "out")
+    st = _lib.load().qlora_moment8_values(0 if moment.signed else 1, n, _ptr(moment.codes), _ptr(moment.steps),
+                                          _ptr(out), _stream(moment.codes.device))
+    _lib.check(st, "qlora_moment8_values")
+    return out
+
+
+class AdamWStep:
+    """Prepared optimizer step over any number of tensors, one launch a step.
+
+    tensors: list of (param fp32, param_bf16 bf16 or None, grad bf16 or fp32, exp_avg, exp_avg_sq), the moments
+    both fp32 tensors or both Moment8 (signed first); each contiguous with the same number of elements, on one GPU
+    or (the gradient too) in pinned host memory.  The tensors' table is written to `device` (the GPU of the
+    tensors, or the current one) here, on the current stream; the tensors must stay where they are.  clip() and
+    run() of one AdamWStep must be ordered.
+    """
+
+    def __init__(self, tensors, device=None):
+        self._keep = list(tensors)
+        if not self._keep:
+            raise ValueError("no tensors")
+        if device is not None:
+            device = torch.device(device)
+            if device.index is None:
+                device = torch.device(device.type, torch.cuda.current_device())
+        arr = (_lib.AdamWTensor * len(self._keep))()
+        for i, (p, p16, g, m, v) in enumerate(self._keep):
+            n = p.numel()
+            eight = isinstance(m, Moment8)
+            if eight != isinstance(v, Moment8):
+                raise TypeError("exp_avg and exp_avg_sq: both Moment8 or neither")
+            named = [(p, "param", torch.float32), (g, "grad", g.dtype)]
+            if p16 is not None:
+                named.append((p16, "param_bf16", torch.bfloat16))
+            if eight:
+                if not m.signed or v.signed:
+                    raise ValueError("exp_avg must be a signed Moment8, exp_avg_sq one that is not")
+                m.check("exp_avg", n)
+                v.check("exp_avg_sq", n)
+                moments = [(m.codes, "exp_avg", None), (m.steps, "exp_avg", None), (v.codes, "exp_avg_sq", None),
+                           (v.steps, "exp_avg_sq", None)]
+            else:
+                moments = [(m, "exp_avg", torch.float32), (v, "exp_avg_sq", torch.float32)]
+                named += moments
+            gtype = _type_of(g, "grad")
+            for t, nm, dtype in named:
+                if t.dtype != dtype:
+                    raise TypeError(f"{nm}: expected {dtype}, got {t.dtype}")
+                if t.numel() != n or not t.is_contiguous():
+                    raise ValueError(f"{nm}: expected {n} contiguous elements")
+            for t, nm, _ in named + moments:
+                if t.is_cuda:
+                    if device is None:
+                        device = t.device
+                    if t.device != device:
+                        raise ValueError(f"{nm}: all tensors must be on {device}, got one on {t.device}")
+                elif not t.is_pinned():
+                    raise ValueError(f"{nm}: must be on the GPU or in pinned host memory")
+            arr[i] = _lib.AdamWTensor(n, _ptr(p), _ptr(p16), _ptr(g), _ptr(m.codes if eight else m),
+                                      _ptr(v.codes if eight else v), _ptr(m.steps) if eight else None,
+                                      _ptr(v.steps) if eight else None, gtype, int(eight))
+        if device is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device = device
+        lib = _lib.load()
+        need = int(lib.qlora_adamw_plan_bytes(arr, len(self._keep)))
+        self._plan = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        self._handle = _lib.AdamWHandle()
+        st = lib.qlora_adamw_plan(arr, len(self._keep), _ptr(self._plan), self._plan.numel(),
+                                  ctypes.byref(self._handle), _stream(self.device))
+        _lib.check(st, "qlora_adamw_plan")
+
+    def clip(self, max_norm: float, out: torch.Tensor | None = None) -> torch.Tensor:
+        """fp32 [2] on the device: the norm of all gradients, and the factor min(1, max_norm / (norm + 1e-6)) that
+        run() takes (NaN where the norm is not finite)."""
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device=self.device)
+        else:
+            _need(out, torch.float32, (2,), "out")
+        st = _lib.load().qlora_grad_clip(ctypes.byref(self._handle), float(max_norm), _ptr(out), _stream(self.device))
+        _lib.check(st, "qlora_grad_clip")
+        return out
+
+    def run(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
+            step: int = 1, clip: torch.Tensor | None = None) -> None:
+        """One step (number `step`, from 1).  clip: what clip() returned, to multiply the gradients by its factor;
+        where that is NaN the step is not taken."""
+        if clip is not None:
+            _need(clip, torch.float32, (2,), "clip")
+        st = _lib.load().qlora_adamw_step(ctypes.byref(self._handle), float(lr), float(beta1), float(beta2),
+                                          float(eps), float(weight_decay), int(step), _ptr(clip),
+                                          _stream(self.device))
+        _lib.check(st, "qlora_adamw_step")
+
+
 def profile_enable(on: bool = True) -> None:
     _lib.check(_lib.load().qlora_profile_enable(1 if on else 0), "qlora_profile_enable")
 

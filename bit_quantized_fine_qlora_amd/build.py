@@ -18,7 +18,7 @@ ROOT = os.path.dirname(PKG_DIR)
 LIB_NAME = "libqlora.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["quantize.hip", "gemm_linear.hip", "gemv_small.hip", "lora.hip", "merge.hip", "adam.hip",
-           "checkpoint.hip", "norm_fwd.hip", "norm_bwd.hip", "preference.hip", "api.hip"]
+           "checkpoint.hip", "norm_fwd.hip", "norm_bwd.hip", "preference.hip", "experts.hip", "adamw.hip", "api.hip"]
 ARCH = "gfx950"
 
 # No packed-fp32 instructions anywhere; no fast-math (the quantizer's

@@ -9,6 +9,8 @@
 #include <vector>
 
 #include "../../include/qlora.h"
+#include "adamw.h"
+#include "experts.h"
 #include "qlora_common.h"
 
 // Scratch of qlora_linear_fwd_static, one copy per device (see static_scratch
@@ -375,6 +377,90 @@ BwdWs bwd_ws(int64_t M, int64_t n, int64_t m, int32_t r, bool dropout = false) {
   w.has_ksplit = kb != 0;
   w.total = L.total;
   return w;
+}
+
+struct ExpertsWs {
+  size_t gpad, Bt, part, u, part_u, v, vplanes, uplanes, gA, gB, pieces, total;
+  int splits, splits_u;  // K splits of u (forward) or v, and of the backward's u
+  int64_t m_pad;
+};
+
+// rows behind B_e^T's: the down product reads B itself where a row of it is
+// whole 16-byte pieces
+bool experts_b_direct(int32_t r) { return r % 8 == 0; }
+
+ExpertsWs experts_ws(bool bwd, int64_t M, int64_t E, int64_t n, int64_t m, int32_t r) {
+  WsLayout L;
+  ExpertsWs w{};
+  w.m_pad = (m % 8 == 0) ? m : ((m + 63) / 64) * 64;
+  const size_t factor = (size_t)M * r * sizeof(float);
+  if (!bwd) {
+    w.splits = experts_down_splits(M, E, n, r);
+    w.part = L.take(w.splits * factor);
+    w.u = L.take(factor);
+    w.pieces = L.take(experts_gemm_ws_bytes(M, E, m, n));
+    w.total = L.total;
+    return w;
+  }
+  w.gpad = m % 8 == 0 ? 0 : L.take((size_t)M * w.m_pad * 2);
+  w.Bt = experts_b_direct(r) ? 0 : L.take((size_t)E * r * w.m_pad * 2);
+  w.splits = experts_down_splits(M, E, w.m_pad, r);
+  w.splits_u = experts_down_splits(M, E, n, r);
+  w.part = L.take(w.splits * factor);
+  w.part_u = L.take(w.splits_u * factor);
+  w.v = L.take(factor);
+  w.vplanes = L.take(experts_planes_bytes(M, r));
+  w.uplanes = L.take(experts_planes_bytes(M, r));
+  w.gA = L.take(experts_token_ws_bytes(M, n, r));
+  w.gB = L.take(experts_token_ws_bytes(M, m, r));
+  w.pieces = L.take(experts_gemm_ws_bytes(M, E, n, w.m_pad));
+  w.total = L.total;
+  return w;
+}
+
+qlora_status check_experts(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s) {
+  const qlora_status st = check_linear(M, n, m, r, s);
+  if (st == QLORA_ERR_SHAPE) return st;
+  if (E < 1 || E > QLORA_MAX_EXPERTS || M >= ((int64_t)1 << 22)) return QLORA_ERR_SHAPE;
+  if (m >= kMaxDim / E || E * m > ((int64_t)1 << 40) / n) return QLORA_ERR_SHAPE;
+  if (!experts_gemm_fits(M, E, n) || !experts_gemm_fits(M, E, m) || !experts_token_fits(M, E, n) ||
+      !experts_token_fits(M, E, m))
+    return QLORA_ERR_SHAPE;
+  return st;
+}
+
+qlora_status check_adamw_tensor(const qlora_adamw_tensor& t) {
+  if (t.count < 1 || t.count >= ((int64_t)1 << 40)) return QLORA_ERR_SHAPE;
+  if ((t.grad_type != QLORA_BF16 && t.grad_type != QLORA_F32) ||
+      (t.moments != QLORA_MOMENTS_F32 && t.moments != QLORA_MOMENTS_8BIT))
+    return QLORA_ERR_VALUE;
+  if (!t.param || !t.grad || !t.exp_avg || !t.exp_avg_sq) return QLORA_ERR_NULL;
+  const bool steps = t.moments == QLORA_MOMENTS_8BIT;
+  if (steps && (!t.exp_avg_steps || !t.exp_avg_sq_steps)) return QLORA_ERR_NULL;
+  if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) || !aligned16(t.exp_avg_sq) ||
+      !aligned16(t.param_bf16) || (steps && (!aligned16(t.exp_avg_steps) || !aligned16(t.exp_avg_sq_steps))))
+    return QLORA_ERR_ALIGN;
+  return QLORA_OK;
+}
+
+// A plan's chunks, or a negative status.
+int64_t adamw_total_chunks(const qlora_adamw_tensor* tensors, int64_t count) {
+  if (!tensors) return QLORA_ERR_NULL;
+  if (count < 1 || count >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const qlora_status st = check_adamw_tensor(tensors[i]);
+    if (st != QLORA_OK) return st;
+    chunks += adamw_chunks(tensors[i].count);
+    if (chunks >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
+  }
+  return chunks;
+}
+
+qlora_status check_adamw_handle(const qlora_adamw_handle* h) {
+  if (!h || !h->plan) return QLORA_ERR_NULL;
+  if (h->tensors < 1 || h->chunks < 1 || h->chunks >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
+  return aligned16(h->plan) ? QLORA_OK : QLORA_ERR_ALIGN;
 }
 
 // Device form of a dropout request; inv_keep = 1 / (1 - p).  NULL or p = 0
@@ -1093,6 +1179,174 @@ qlora_status qlora_preference_bwd(int32_t type, int64_t T, int64_t V, const void
   {
     Timed tm("preference_bwd", hs);
     launch_pref_grad(type, T, V, logits, labels, lse, coef, grad_scale, grad_logits, hs);
+  }
+  return hip_status();
+}
+
+size_t qlora_experts_workspace_bytes(int op, int64_t M, int64_t E, int64_t n, int64_t m, int32_t r) {
+  if (op != QLORA_OP_FWD && op != QLORA_OP_BWD) return 0;
+  if (check_experts(M, E, n, m, r, 1.0f) != QLORA_OK) return 0;
+  return experts_ws(op == QLORA_OP_BWD, M, E, n, m, r).total;
+}
+
+qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
+                               const int32_t* offsets, const uint8_t* codes, const uint8_t* absmax8, const float* c2,
+                               const qlora_bf16* A, const qlora_bf16* B, qlora_bf16* h, float* u_out,
+                               void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  const qlora_status st = check_experts(M, E, n, m, r, s);
+  if (st != QLORA_OK) return st;
+  if (!x || !offsets || !codes || !absmax8 || !c2 || !A || !B || !h) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(offsets) || !aligned16(codes) || !aligned16(absmax8) || !aligned16(c2) ||
+      !aligned16(A) || !aligned16(B) || !aligned16(h) || !aligned16(u_out))
+    return QLORA_ERR_ALIGN;
+  const ExpertsWs w = experts_ws(false, M, E, n, m, r);
+  if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  float* const u = u_out ? u_out : at<float>(workspace, w.u);
+  {
+    Timed tm("experts_down", hs);
+    float* const part = at<float>(workspace, w.part);
+    launch_experts_down(x, offsets, M, E, n, A, false, n, r, part, w.splits, hs);
+    const FactorJob job{part, w.splits, u, nullptr};
+    launch_experts_factor(&job, 1, offsets, M, E, r, hs);
+  }
+  {
+    Timed tm("experts_fwd_gemm", hs);
+    launch_experts_gemm(false, offsets, E, x, codes, absmax8, c2, B, u, h, M, n, n, m, r, s,
+                        at<uint8_t>(workspace, w.pieces), table(), hs);
+  }
+  return hip_status();
+}
+
+qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
+                               const qlora_bf16* g, const int32_t* offsets, const uint8_t* codes,
+                               const uint8_t* absmax8, const float* c2, const qlora_bf16* A, const qlora_bf16* B,
+                               const float* u, qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
+                               void* workspace, size_t workspace_bytes, qlora_stream_t stream) {
+  const qlora_status st = check_experts(M, E, n, m, r, s);
+  if (st != QLORA_OK) return st;
+  if (!x || !g || !offsets || !codes || !absmax8 || !c2 || !A || !B || !grad_A || !grad_B) return QLORA_ERR_NULL;
+  if (!aligned16(x) || !aligned16(g) || !aligned16(offsets) || !aligned16(codes) || !aligned16(absmax8) ||
+      !aligned16(c2) || !aligned16(A) || !aligned16(B) || !aligned16(u) || !aligned16(grad_x) ||
+      !aligned16(grad_A) || !aligned16(grad_B))
+    return QLORA_ERR_ALIGN;
+  const ExpertsWs w = experts_ws(true, M, E, n, m, r);
+  if (!workspace || workspace_bytes < w.total) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  float* const v = at<float>(workspace, w.v);
+  const uint16_t* gk = g;
+  if (w.m_pad != m) {
+    Timed tm("transpose", hs);
+    uint16_t* const gp = at<uint16_t>(workspace, w.gpad);
+    launch_pad_cols_bf16(g, M, m, w.m_pad, gp, hs);
+    gk = gp;
+  }
+  const bool direct = experts_b_direct(r);
+  if (!direct) {
+    Timed tm("transpose", hs);
+    launch_experts_transpose(B, E, m, r, w.m_pad, at<uint16_t>(workspace, w.Bt), hs);
+  }
+  uint16_t* const vplanes = at<uint16_t>(workspace, w.vplanes);
+  uint16_t* const uplanes = at<uint16_t>(workspace, w.uplanes);
+  {
+    Timed tm("experts_down", hs);
+    float* const part = at<float>(workspace, w.part);
+    launch_experts_down(gk, offsets, M, E, w.m_pad, direct ? B : at<uint16_t>(workspace, w.Bt), direct,
+                        direct ? m : w.m_pad, r, part, w.splits, hs);
+    FactorJob jobs[2] = {{part, w.splits, grad_x ? v : nullptr, vplanes}, {u, 1, nullptr, uplanes}};
+    if (!u) {
+      float* const part_u = at<float>(workspace, w.part_u);
+      launch_experts_down(x, offsets, M, E, n, A, false, n, r, part_u, w.splits_u, hs);
+      jobs[1] = FactorJob{part_u, w.splits_u, nullptr, uplanes};
+    }
+    launch_experts_factor(jobs, 2, offsets, M, E, r, hs);
+  }
+  if (grad_x) {
+    Timed tm("experts_dgrad_gemm", hs);
+    launch_experts_gemm(true, offsets, E, gk, codes, absmax8, c2, A, v, grad_x, M, w.m_pad, n, m, r, s,
+                        at<uint8_t>(workspace, w.pieces), table(), hs);
+  }
+  {
+    Timed tm("experts_token", hs);
+    launch_experts_token(x, vplanes, grad_A, at<float>(workspace, w.gA), gk, w.m_pad, uplanes, grad_B,
+                         at<float>(workspace, w.gB), offsets, M, E, n, m, r, s, hs);
+  }
+  return hip_status();
+}
+
+size_t qlora_adamw_plan_bytes(const qlora_adamw_tensor* tensors, int64_t count) {
+  const int64_t chunks = adamw_total_chunks(tensors, count);
+  return chunks < 0 ? 0 : adamw_plan_bytes(chunks, count);
+}
+
+qlora_status qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t count, void* plan, size_t plan_bytes,
+                              qlora_adamw_handle* handle, qlora_stream_t stream) {
+  const int64_t chunks = adamw_total_chunks(tensors, count);
+  if (chunks < 0) return (qlora_status)chunks;
+  if (!handle) return QLORA_ERR_NULL;
+  if (!plan || plan_bytes < adamw_plan_bytes(chunks, count)) return QLORA_ERR_WORKSPACE;
+  if (!aligned16(plan)) return QLORA_ERR_ALIGN;
+  AdamWTensor ts[kPlanPerLaunch];
+  int64_t chunk = 0;
+  for (int64_t i = 0; i < count; i += kPlanPerLaunch) {
+    const int batch = (int)(count - i < kPlanPerLaunch ? count - i : kPlanPerLaunch);
+    for (int k = 0; k < batch; ++k) {
+      const qlora_adamw_tensor& t = tensors[i + k];
+      ts[k] = AdamWTensor{t.count, t.param, t.param_bf16, t.grad, t.exp_avg, t.exp_avg_sq, t.exp_avg_steps,
+                          t.exp_avg_sq_steps, chunk, t.grad_type, t.moments};
+      chunk += adamw_chunks(t.count);
+    }
+    launch_adamw_plan(ts, i, batch, count, chunks, plan, reinterpret_cast<hipStream_t>(stream));
+  }
+  const qlora_status st = hip_status();
+  if (st == QLORA_OK) *handle = qlora_adamw_handle{plan, count, chunks, 0};
+  return st;
+}
+
+qlora_status qlora_grad_clip(const qlora_adamw_handle* handle, double max_norm, float* out, qlora_stream_t stream) {
+  const qlora_status st = check_adamw_handle(handle);
+  if (st != QLORA_OK) return st;
+  if (!(max_norm > 0.0)) return QLORA_ERR_VALUE;
+  if (!out) return QLORA_ERR_NULL;
+  if (!aligned16(out)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("grad_clip", hs);
+    launch_grad_clip(handle->plan, handle->tensors, handle->chunks, max_norm, out, hs);
+  }
+  return hip_status();
+}
+
+qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
+                              double weight_decay, int64_t step, const float* clip, qlora_stream_t stream) {
+  const qlora_status st = check_adamw_handle(handle);
+  if (st != QLORA_OK) return st;
+  if (step < 1 || !std::isfinite(lr) || lr < 0.0 || !std::isfinite(eps) || (float)eps < 1.17549435e-38f ||
+      !std::isfinite((float)eps) || !std::isfinite(weight_decay) || !(beta1 >= 0.0 && beta1 < 1.0) ||
+      !(beta2 >= 0.0 && beta2 < 1.0))
+    return QLORA_ERR_VALUE;
+  if (!aligned16(clip)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("adamw", hs);
+    launch_adamw_step(handle->plan, handle->tensors, handle->chunks, lr, beta1, beta2, eps, weight_decay, step, clip,
+                      hs);
+  }
+  return hip_status();
+}
+
+qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* codes, const float* steps, float* out,
+                                  qlora_stream_t stream) {
+  if (second != 0 && second != 1) return QLORA_ERR_VALUE;
+  if (count < 1 || count >= ((int64_t)1 << 40)) return QLORA_ERR_SHAPE;
+  if (!codes || !steps || !out) return QLORA_ERR_NULL;
+  if (!aligned16(codes) || !aligned16(steps) || !aligned16(out)) return QLORA_ERR_ALIGN;
+  hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+  {
+    Timed tm("moment8_values", hs);
+    launch_moment8_values(second == 0, count, codes, steps, out, hs);
   }
   return hip_status();
 }

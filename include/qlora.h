@@ -7,7 +7,8 @@
  *   - the adapted forward  h = x W'^T + s (x A^T) B^T,  W' = dequant(W0);
  *   - its backward through the frozen 4-bit weight: grad_x, grad_A, grad_B;
  * and what stands next to it in a training step: the norm in front of the
- * layer, its input kept in 8 bits for the backward pass, and a preference loss.
+ * layer, its input kept in 8 bits for the backward pass, a preference loss, the
+ * layer over the rows of many experts, and the optimizer step of the adapters.
  * Sources are the QLoRA pages cited at each entry point below.
  *
  * Conventions for every call:
@@ -556,6 +557,135 @@ qlora_status qlora_preference_bwd(int32_t type, int64_t T, int64_t V, const void
                                   qlora_stream_t stream);
 
 /*
+ * The adapted layer of many experts: the M rows of x belong to E experts, each
+ * with a frozen weight and an adapter of its own, in order of their expert
+ * ("QLoRA: Efficient Fine-Tuning", Step 3, Eq. 3, for each expert's rows):
+ *   rows offsets[e] .. offsets[e + 1] - 1:
+ *   u = x A_e^T                    (fp32 accumulation)
+ *   h = bf16(x W'_e^T + s u B_e^T)
+ *   offsets  device, E + 1 int32, ascending.  An expert may have no row.  Rows
+ *            before offsets[0] or from offsets[E] on belong to no expert: they
+ *            are not read, and their rows of h, u_out and grad_x stay as they
+ *            were.  Values outside 0 .. M are held within it, one below an
+ *            earlier one counts as that one.
+ *   codes, absmax8, c2: the experts' m x n weights as one quantized E m x n
+ *            weight, expert e's rows e m .. (e + 1) m - 1.
+ *   A        device, E x r x n bf16.      B  device, E x m x r bf16.
+ *   x, h, u_out: as for qlora_linear_fwd, M rows in all; u_out may be NULL.
+ * Requires 1 <= E <= 1024, M < 2^22, E m < 2^31, E m n <= 2^40, and for each
+ * expert the limits of qlora_linear_fwd with all M rows.  No dropout.
+ */
+#define QLORA_MAX_EXPERTS 1024
+qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
+                               const int32_t* offsets, const uint8_t* codes, const uint8_t* absmax8, const float* c2,
+                               const qlora_bf16* A, const qlora_bf16* B, qlora_bf16* h, float* u_out,
+                               void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/*
+ * Workspace bytes of qlora_experts_fwd (op QLORA_OP_FWD) and
+ * qlora_experts_bwd (QLORA_OP_BWD); 0 on invalid arguments.
+ */
+size_t qlora_experts_workspace_bytes(int op, int64_t M, int64_t E, int64_t n, int64_t m, int32_t r);
+
+/*
+ * Backward of qlora_experts_fwd for the upstream gradient g = dL/dh ("QLoRA:
+ * Efficient Fine-Tuning", Step 4 and Eq. 5), each over its expert's rows:
+ *   v      = g B_e,   grad_x = bf16(g W'_e + s v A_e)      (M x n)
+ *   grad_A_e = bf16(s v^T x)   (E x r x n),   grad_B_e = bf16(s g^T u)   (E x m x r)
+ * zeros for an expert without rows.  u: the forward's u_out, or NULL to
+ * recompute it; grad_x: NULL to skip it.  Sums over rows go through fp32
+ * partials in a fixed order: results are bit-identical run to run.
+ */
+qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
+                               const qlora_bf16* g, const int32_t* offsets, const uint8_t* codes,
+                               const uint8_t* absmax8, const float* c2, const qlora_bf16* A, const qlora_bf16* B,
+                               const float* u, qlora_bf16* grad_x, qlora_bf16* grad_A, qlora_bf16* grad_B,
+                               void* workspace, size_t workspace_bytes, qlora_stream_t stream);
+
+/* How a tensor's moments are kept. */
+#define QLORA_MOMENTS_F32 0
+#define QLORA_MOMENTS_8BIT 1
+
+/*
+ * One tensor of qlora_adamw_step (host struct; device-addressable pointers, as
+ * for qlora_adam_tensor; grad in device memory or pinned host memory).
+ *   count       elements (>= 1, < 2^40).
+ *   param       fp32 master weights, updated in place.
+ *   param_bf16  bf16 copy written after the update, or NULL.
+ *   grad        gradient of grad_type, QLORA_BF16 or QLORA_F32.
+ *   moments     QLORA_MOMENTS_F32: exp_avg and exp_avg_sq are `count` floats,
+ *               the steps NULL.  QLORA_MOMENTS_8BIT: `count` bytes each, with
+ *               ceil(count / 128) floats of steps; all zero before the first
+ *               step ("QLoRA & 4-bit Fine-Tuning", Innovation 3: what is left
+ *               to shrink once the weight has 4 bits is optimizer state).
+ * An 8-bit moment: 128 consecutive elements share a step d.  exp_avg: bit 7 is
+ * the sign, k = bits 0-6, the value +-k^2 d with d = fp32(largest / 127^2).
+ * exp_avg_sq: its root is k^2 d, k = 0 .. 255, the value that squared, d =
+ * fp32(largest root / 255^2); a value that is not 0 takes k >= 1.  Each value
+ * takes the nearest of them, of two as near the lower, decided in 64 bits; a d
+ * below 2^-126 is 0, and all of its block.
+ * Every pointer 16-byte aligned; tensors must not overlap.
+ */
+typedef struct {
+  int64_t count;
+  float* param;
+  qlora_bf16* param_bf16;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_steps;
+  float* exp_avg_sq_steps;
+  int32_t grad_type;
+  int32_t moments;
+} qlora_adamw_tensor;
+
+/*
+ * The plan of steps over `count` tensors (any number of them): their table in
+ * device memory, written once, after which a step is one launch.  plan_bytes
+ * of at least qlora_adamw_plan_bytes (0 on invalid arguments), 16-byte
+ * aligned.  `tensors` is a host array read before the call returns.  The plan
+ * also holds the sums of qlora_grad_clip: calls on one plan must be ordered.
+ * Writes 32 bytes of host memory at `handle`, which the calls below take.
+ */
+typedef struct {
+  void* plan;
+  int64_t tensors;
+  int64_t chunks;
+  int64_t reserved;
+} qlora_adamw_handle;
+size_t qlora_adamw_plan_bytes(const qlora_adamw_tensor* tensors, int64_t count);
+qlora_status qlora_adamw_plan(const qlora_adamw_tensor* tensors, int64_t count, void* plan, size_t plan_bytes,
+                              qlora_adamw_handle* handle, qlora_stream_t stream);
+
+/*
+ * Norm of the plan's gradients over all tensors, and the factor that holds it
+ * to max_norm (> 0; infinity only measures):
+ *   out[0] = sqrt(sum of squares), out[1] = min(1, max_norm / (out[0] + 1e-6))
+ * out: device, 2 fp32.  Squares and sums in 64 bits, in a fixed order.  Where
+ * the norm is not finite out[1] is NaN.
+ */
+qlora_status qlora_grad_clip(const qlora_adamw_handle* handle, double max_norm, float* out, qlora_stream_t stream);
+
+/*
+ * Adam step with decoupled weight decay over the plan's tensors, in one
+ * launch, as qlora_adam_step with each gradient multiplied by clip[1] first
+ * (clip: device, the output of qlora_grad_clip, or NULL for 1).  A factor
+ * that is not finite takes no step: nothing is written.  8-bit moments are
+ * formed in 64 bits and the weight's update reads them before their rounding.
+ * Hyperparameters as there, eps at least 2^-126 in fp32.  With 8-bit moments
+ * gradients must be finite (checked by a clip); fp32 moments as there.
+ */
+qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
+                              double weight_decay, int64_t step, const float* clip, qlora_stream_t stream);
+
+/*
+ * The fp32 values that an 8-bit moment's `count` codes stand for; second: 0
+ * for an exp_avg, 1 for an exp_avg_sq.
+ */
+qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* codes, const float* steps, float* out,
+                                  qlora_stream_t stream);
+
+/*
  * Completion check of the last qlora_linear_fwd / qlora_linear_bwd(_ex)
  * call (op QLORA_OP_FWD, QLORA_OP_BWD or QLORA_OP_BWD_DROPOUT) that used
  * `workspace` with these sizes.  When a GEMM has more output tiles than the
@@ -582,7 +712,9 @@ qlora_status qlora_linear_check(int op, int64_t M, int64_t n, int64_t m, int32_t
  * ("quantize", "dequant", "fwd_gemm", "fwd_small", "dgrad_gemm",
  * "down_proj", "token_grad", "transpose", "gpass", "dropout_term", "merge",
  * "adam", "checkpoint_pack", "checkpoint_unpack", "norm_fwd", "norm_bwd",
- * "preference_fwd", "preference_bwd") and reports the launch
+ * "preference_fwd", "preference_bwd", "experts_down", "experts_fwd_gemm",
+ * "experts_dgrad_gemm", "experts_token", "grad_clip", "adamw",
+ * "moment8_values") and reports the launch
  * count and the summed duration in milliseconds (host pointers).
  */
 qlora_status qlora_profile_enable(int on);
