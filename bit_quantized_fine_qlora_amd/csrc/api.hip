@@ -260,6 +260,7 @@ struct Timed {
 // checks
 // ---------------------------------------------------------------------------
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int64_t kMaxDim = (int64_t)1 << 31;
 
@@ -398,7 +399,8 @@ ExpertsWs experts_ws(bool bwd, int64_t M, int64_t E, int64_t n, int64_t m, int32
     w.splits = experts_down_splits(M, E, n, r);
     w.part = L.take(w.splits * factor);
     w.u = L.take(factor);
-    w.pieces = L.take(experts_gemm_ws_bytes(M, E, m, n));
+    w.pieces = L.take(experts_stream_takes(M, E, m, n) ? experts_stream_ws_bytes(M, E, m, n)
+                                                       : experts_gemm_ws_bytes(M, E, m, n));
     w.total = L.total;
     return w;
   }
@@ -438,7 +440,7 @@ qlora_status check_adamw_tensor(const qlora_adamw_tensor& t) {
   const bool steps = t.moments == QLORA_MOMENTS_8BIT;
   if (steps && (!t.exp_avg_steps || !t.exp_avg_sq_steps)) return QLORA_ERR_NULL;
   if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.exp_avg) || !aligned16(t.exp_avg_sq) ||
-      !aligned16(t.param_bf16) || (steps && (!aligned16(t.exp_avg_steps) || !aligned16(t.exp_avg_sq_steps))))
+      !aligned16(t.param_bf16) || (steps && (!aligned4(t.exp_avg_steps) || !aligned4(t.exp_avg_sq_steps))))
     return QLORA_ERR_ALIGN;
   return QLORA_OK;
 }
@@ -1208,6 +1210,11 @@ qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
     Timed tm("experts_down", hs);
     float* const part = at<float>(workspace, w.part);
     launch_experts_down(x, offsets, M, E, n, A, false, n, r, part, w.splits, hs);
+    if (experts_stream_takes(M, E, m, n)) {
+      launch_experts_stream(offsets, E, x, codes, absmax8, c2, B, part, w.splits, u_out, h, M, n, m, r, s,
+                            at<uint8_t>(workspace, w.pieces), table(), hs);
+      return hip_status();
+    }
     const FactorJob job{part, w.splits, u, nullptr};
     launch_experts_factor(&job, 1, offsets, M, E, r, hs);
   }
@@ -1342,7 +1349,7 @@ qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* 
   if (second != 0 && second != 1) return QLORA_ERR_VALUE;
   if (count < 1 || count >= ((int64_t)1 << 40)) return QLORA_ERR_SHAPE;
   if (!codes || !steps || !out) return QLORA_ERR_NULL;
-  if (!aligned16(codes) || !aligned16(steps) || !aligned16(out)) return QLORA_ERR_ALIGN;
+  if (!aligned16(codes) || !aligned4(steps) || !aligned16(out)) return QLORA_ERR_ALIGN;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
   {
     Timed tm("moment8_values", hs);

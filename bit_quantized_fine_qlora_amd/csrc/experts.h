@@ -20,6 +20,12 @@ void launch_experts_gemm(bool bwd, const int32_t* offsets, int64_t E, const uint
                          const uint8_t* absmax8, const float* c2, const uint16_t* lora_a, const float* lora_b,
                          uint16_t* out, int64_t M, int64_t K, int64_t n, int64_t m, int r, float s, void* ws,
                          const Nf4Table& tab, hipStream_t stream);
+size_t experts_stream_ws_bytes(int64_t M, int64_t E, int64_t N, int64_t K);
+bool experts_stream_takes(int64_t M, int64_t E, int64_t N, int64_t K);
+void launch_experts_stream(const int32_t* offsets, int64_t E, const uint16_t* x, const uint8_t* codes,
+                           const uint8_t* absmax8, const float* c2, const uint16_t* B, const float* u, int usplits,
+                           float* u_out, uint16_t* h, int64_t M, int64_t n, int64_t m, int r, float s, void* ws,
+                           const Nf4Table& tab, hipStream_t stream);
 int experts_down_splits(int64_t M, int64_t E, int64_t K, int R);
 void launch_experts_down(const uint16_t* X, const int32_t* offsets, int64_t M, int64_t E, int64_t K, const uint16_t* Y,
                          bool yt, int64_t yrows, int R, float* part, int splits, hipStream_t stream);

@@ -134,6 +134,51 @@ __device__ __forceinline__ bool find_span(const ExpertRows& r, int bt, Pick pick
   return true;
 }
 
+// The same with the tiles numbered whole ones first and then each expert's
+// ragged last one: a launch then ends with its short tiles.  pick(whole,
+// ragged) names a tile of whole + ragged.
+template <typename Pick>
+__device__ __forceinline__ bool find_span_whole_first(const ExpertRows& r, int bt, Pick pick, Span& s) {
+  auto counts = [&](const ExpertScan& k, int& w, int& g) {  // of the lanes up to this one
+    const int whole = k.rows / bt;
+    g = __popcll(__ballot(k.t > whole) & (~0ull >> (63 - (threadIdx.x & 63))));
+    w = k.t_incl - g;
+  };
+  ExpertScan k;
+  k.begin(r);
+  k.load(r, bt);
+  int w, g, whole = 0, ragged = 0;
+  for (;;) {
+    counts(k, w, g);
+    whole += __builtin_amdgcn_readlane(w, 63);
+    ragged += __builtin_amdgcn_readlane(g, 63);
+    if (k.first + 64 >= r.E) break;
+    k.next(r);
+    k.load(r, bt);
+  }
+  const int item = __builtin_amdgcn_readfirstlane(pick(whole, ragged));
+  if (item < 0 || item >= whole + ragged) return false;
+  const bool last = item >= whole;
+  int want = last ? item - whole : item;  // among the tiles of its kind
+  if (r.E > 64) {
+    k.begin(r);
+    k.load(r, bt);
+    counts(k, w, g);
+    for (;;) {
+      const int here = __builtin_amdgcn_readlane(last ? g : w, 63);
+      if (want < here) break;
+      want -= here;
+      k.next(r);
+      k.load(r, bt);
+      counts(k, w, g);
+    }
+  }
+  const int lane = __builtin_ctzll(__ballot((last ? g : w) > want));
+  const int full = __builtin_amdgcn_readlane(k.rows / bt, lane);
+  s = k.span(lane, last ? full : want - (__builtin_amdgcn_readlane(w, lane) - full));
+  return true;
+}
+
 // Expert e's rows and tiles (its first).
 __device__ __forceinline__ Span expert_span(const ExpertRows& r, int bt, int e) {
   ExpertScan k;
@@ -146,14 +191,44 @@ __device__ __forceinline__ Span expert_span(const ExpertRows& r, int bt, int e) 
   return k.span(e - k.first, 0);
 }
 
+// The rows that belong to an expert: offsets[0] .. the largest offset, within
+// 0 .. M.
+__device__ __forceinline__ void live_rows(const ExpertRows& r, int& low, int& top) {
+  top = 0;
+  for (int e = threadIdx.x & 63; e <= r.E; e += 64) {
+    const int o = r.offsets[e];
+    top = o > top ? o : top;
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) {
+    const int o = __shfl_xor(top, d, 64);
+    top = o > top ? o : top;
+  }
+  top = top < r.M ? top : r.M;
+  low = ExpertScan::held(r.offsets[0], r.M);
+}
+
 // Most tiles of bt rows that M rows of E experts make.
 static inline int64_t most_tiles(int64_t M, int64_t E, int64_t bt) { return M / bt + (E < M ? E : M); }
 
 // ---------------------------------------------------------------------------
 // h and grad_x: the dense GEMM's tile on an expert's operands
 // ---------------------------------------------------------------------------
+// Few tiles run as K pieces, as in the dense layer: a piece to each of `slots`
+// workgroups (0: no pieces), with at least 8 K steps.  How many tiles there are
+// is only known here, so where there may be enough of them to go without, both
+// kernels are launched, and one of them ends at once (a kernel that could do
+// either would not have the registers).
+__device__ __forceinline__ int pieces_of(int tiles, int slots, int nk) {
+  int p = slots / (tiles > 0 ? tiles : 1);
+  p = p < 16 ? p : 16;
+  p = p < nk / 8 ? p : nk / 8;
+  return p > 1 ? p : 1;
+}
+
 template <bool kBwd, bool kPieces>
-__global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p, ExpertRows er, Nf4Table tab) {
+__global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p, ExpertRows er, Nf4Table tab,
+                                                                     int slots) {
   using T = lg2::Tile<kBwd>;
   __shared__ __align__(16) uint8_t sw0[T::W];
   __shared__ __align__(16) uint8_t sw1[T::W];
@@ -162,30 +237,36 @@ __global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p,
   __shared__ uint32_t lds_word;
   const lg2::Lds lds{{sw0, sw1}, {sa0, sa1}};
   const int tid = threadIdx.x;
-  int k0 = 0, ks = (int)((p.K + lg2::BK - 1) / lg2::BK);
-  bool lora = true;
-  int bid = (int)blockIdx.x;
-  if (kPieces) {
-    const int piece = bid % p.pieces;
-    bid /= p.pieces;
-    const int nk = ks;
-    k0 = piece * nk / p.pieces;
-    ks = (piece + 1) * nk / p.pieces - k0;
-    lora = piece == p.pieces - 1;
-  }
+  const int nk = (int)((p.K + lg2::BK - 1) / lg2::BK);
   // Row tiles are numbered through the experts, feature tiles fastest; each
-  // XCD (workgroup number mod 8) takes a run of neighbouring tiles.
-  int tile_f = 0;
+  // XCD (workgroup number mod 8) takes a run of neighbouring tiles, of the
+  // whole ones first and then of the ragged ones.  As pieces: workgroup
+  // piece + pieces tile.
+  const int bid = (int)blockIdx.x;
+  int tile_f = 0, pieces = 1;
   Span s;
-  const bool found = find_span(er, lg2::BT, [&](int total) {
-    const int tiles = total * p.tiles_f;
-    int item = bid;
-    if (!kPieces) {
-      const int run = (tiles + 7) >> 3;
-      item = (bid >> 3) < run ? (bid & 7) * run + (bid >> 3) : tiles;
+  const bool found = find_span_whole_first(er, lg2::BT, [&](int whole, int ragged) {
+    const int first = whole * p.tiles_f, second = ragged * p.tiles_f;
+    int item;
+    pieces = pieces_of(first + second, slots, nk);
+    if (kPieces != (pieces > 1)) return -1;
+    if (kPieces) {
+      item = bid / pieces;
+      if (item >= first + second) return -1;
+    } else {
+      const int run = (first + 7) >> 3, run2 = (second + 7) >> 3;
+      const int k = (bid >> 3) - run;
+      if (k < 0) {
+        item = (bid & 7) * run + (bid >> 3);
+        if (item >= first) return -1;
+      } else {
+        item = (bid & 7) * run2 + k;
+        if (k >= run2 || item >= second) return -1;
+        item += first;
+      }
     }
     tile_f = item % p.tiles_f;
-    return item < tiles ? item / p.tiles_f : -1;
+    return item / p.tiles_f;
   }, s);
   if (!found) return;
   const int64_t cells = p.wm * p.wn;
@@ -199,36 +280,43 @@ __global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p,
   p.lora_b += (int64_t)s.row0 * p.r;
   p.out += s.row0 * p.N;
   p.M = s.rows;
+  pieces = kPieces ? __builtin_amdgcn_readfirstlane(pieces) : 1;
+  tile_f = __builtin_amdgcn_readfirstlane(tile_f);
+  const int piece = kPieces ? bid % pieces : 0;
+  const int k0 = piece * nk / pieces, ks = (piece + 1) * nk / pieces - k0;
+  const bool lora = piece == pieces - 1;
   const int64_t f0 = (int64_t)tile_f * lg2::BF;
   const int64_t t0 = (int64_t)s.tile * lg2::BT;
+  const int64_t left = p.M - t0;
   if (tid >= 64 * lg2::kMfmaWaves)
     gemm_producer<kBwd>(p, tab, lds, tid - 64 * lg2::kMfmaWaves, f0, t0, k0, ks, lora, 0, &lds_word, skew);
-  else
+  else if (left >= lg2::BT)
+    gemm_consumer<kBwd, kPieces, false>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+  else if (left > 128)
     gemm_consumer<kBwd, kPieces, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+  else if (left > 64)
+    gemm_consumer<kBwd, kPieces, false, 128>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+  else
+    gemm_consumer<kBwd, kPieces, false, 64>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
 }
 
 // Finishes tiles that ran as K pieces: out = bf16(piece 0 + piece 1 + ...), in
 // the consumer's [wave][i][j][lane] order, 256 items of 4 features a workgroup.
-template <bool kBwd>
-__global__ __launch_bounds__(256) void experts_pieces_kernel(GemmArgs p, ExpertRows er) {
-  constexpr int WF = kBwd ? 64 : 128;
-  constexpr int WT = 128 * 64 / WF;
+template <bool kBwd, int kRows>
+__device__ __forceinline__ void experts_pieces_tile(const GemmArgs& p, const Span& s, int tile, int rem) {
+  constexpr int WF = WaveTile<kBwd, kRows>::F, WT = WaveTile<kBwd, kRows>::T;
   constexpr int NI = WF / 16, NJ = WT / 16;
-  constexpr int kItems = lg2::BF * lg2::BT / 4;
-  const int tile = (int)blockIdx.x / (kItems / 256);
-  const int rem = ((int)blockIdx.x % (kItems / 256)) * 256 + (int)threadIdx.x;
-  Span s;
-  if (!find_span(er, lg2::BT, [&](int total) { return tile < total * p.tiles_f ? tile / p.tiles_f : -1; }, s)) return;
   const int wave = rem / (NI * NJ * 64);
   const int ij = (rem / 64) % (NI * NJ);
   const int lane = rem % 64;
   const int i = ij / NJ, j = ij % NJ;
   const int64_t t = (int64_t)s.tile * lg2::BT + (wave / (lg2::BF / WF)) * WT + 16 * j + (lane & 15);
   const int64_t f = (int64_t)(tile % p.tiles_f) * lg2::BF + (wave % (lg2::BF / WF)) * WF + 16 * i + 4 * (lane >> 4);
-  if (t >= s.rows || f >= p.N) return;
-  const float* slot = p.piece_out + (size_t)tile * p.pieces * kItems * 4 + (size_t)rem * 4;
+  if (wave >= lg2::kMfmaWaves || t >= s.rows || f >= p.N) return;
+  constexpr size_t kSlot = (size_t)lg2::BF * lg2::BT;
+  const float* slot = p.piece_out + (size_t)tile * p.pieces * kSlot + (size_t)rem * 4;
   f32x4 v = *reinterpret_cast<const f32x4*>(slot);
-  for (int q = 1; q < p.pieces; ++q) v += *reinterpret_cast<const f32x4*>(slot + (size_t)q * kItems * 4);
+  for (int q = 1; q < p.pieces; ++q) v += *reinterpret_cast<const f32x4*>(slot + (size_t)q * kSlot);
   uint16_t* dst = p.out + (s.row0 + t) * p.N + f;
   const u32x2 w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
   if ((p.N & 3) == 0) {
@@ -240,24 +328,42 @@ __global__ __launch_bounds__(256) void experts_pieces_kernel(GemmArgs p, ExpertR
   }
 }
 
-// K pieces of a GEMM with at most `tiles` tiles: as for the dense layer, up to
-// a workgroup a CU, with at least 8 K steps to a piece.
-static int experts_pieces(int64_t tiles, int64_t K) {
-  const int64_t nk = cdiv(K, lg2::BK);
-  int64_t pc = device_cus() / tiles;
-  if (pc > 16) pc = 16;
-  while (pc > 1 && nk / pc < 8) --pc;
-  return pc < 1 ? 1 : (int)pc;
+template <bool kBwd>
+__global__ __launch_bounds__(256) void experts_pieces_kernel(GemmArgs p, ExpertRows er, int slots) {
+  constexpr int kGroups = lg2::BF * lg2::BT / 4 / 256;
+  const int tile = (int)blockIdx.x / kGroups;
+  const int rem = ((int)blockIdx.x % kGroups) * 256 + (int)threadIdx.x;
+  Span s;
+  int pieces = 1;
+  const bool found = find_span_whole_first(er, lg2::BT, [&](int whole, int ragged) {
+    pieces = pieces_of((whole + ragged) * p.tiles_f, slots, (int)((p.K + lg2::BK - 1) / lg2::BK));
+    return pieces > 1 ? tile / p.tiles_f : -1;
+  }, s);
+  if (!found) return;
+  p.pieces = __builtin_amdgcn_readfirstlane(pieces);
+  const int left = s.rows - s.tile * lg2::BT;
+  if (left > 128)
+    experts_pieces_tile<kBwd, 256>(p, s, tile, rem);
+  else if (left > 64)
+    experts_pieces_tile<kBwd, 128>(p, s, tile, rem);
+  else
+    experts_pieces_tile<kBwd, 64>(p, s, tile, rem);
 }
 
 static int64_t gemm_tiles(int64_t M, int64_t E, int64_t N) { return most_tiles(M, E, lg2::BT) * cdiv(N, lg2::BF); }
 
 bool experts_gemm_fits(int64_t M, int64_t E, int64_t N) { return gemm_tiles(M, E, N) < ((int64_t)1 << 24); }
 
+// Workgroups for K pieces: none where there will hardly be as few tiles as
+// half the CUs (the bound counts a ragged tile to every expert), or where K is
+// too short for two.
+static int pieces_slots(int64_t M, int64_t E, int64_t N, int64_t K) {
+  return gemm_tiles(M, E, N) <= device_cus() && cdiv(K, lg2::BK) >= 16 ? device_cus() : 0;
+}
+
+// tiles x pieces is at most the CUs where there are pieces
 size_t experts_gemm_ws_bytes(int64_t M, int64_t E, int64_t N, int64_t K) {
-  const int64_t tiles = gemm_tiles(M, E, N);
-  const int pc = experts_pieces(tiles, K);
-  return pc > 1 ? (size_t)(tiles * pc) * lg2::BF * lg2::BT * sizeof(float) : 0;
+  return (size_t)pieces_slots(M, E, N, K) * lg2::BF * lg2::BT * sizeof(float);
 }
 
 // bwd: act = g (M x K, K = m or m rounded up to 64 with zero columns), out =
@@ -272,25 +378,387 @@ void launch_experts_gemm(bool bwd, const int32_t* offsets, int64_t E, const uint
   p.tiles_f = (int)cdiv(p.N, lg2::BF);
   const ExpertRows er{offsets, (int)E, (int)M};
   const int64_t tiles = gemm_tiles(M, E, p.N);
+  const int slots = pieces_slots(M, E, p.N, K);
   const dim3 block(lg2::kThreads);
-  p.pieces = experts_pieces(tiles, K);
-  if (p.pieces > 1) {
-    p.piece_out = static_cast<float*>(ws);
-    const dim3 grid((unsigned)(tiles * p.pieces)), rgrid((unsigned)(tiles * (lg2::BF * lg2::BT / 4 / 256)));
-    if (bwd) {
-      hipLaunchKernelGGL((experts_gemm_kernel<true, true>), grid, block, 0, stream, p, er, tab);
-      hipLaunchKernelGGL(experts_pieces_kernel<true>, rgrid, dim3(256), 0, stream, p, er);
-    } else {
-      hipLaunchKernelGGL((experts_gemm_kernel<false, true>), grid, block, 0, stream, p, er, tab);
-      hipLaunchKernelGGL(experts_pieces_kernel<false>, rgrid, dim3(256), 0, stream, p, er);
+  // the runs of whole and of ragged tiles are each rounded up to 8
+  const int64_t wgs = cdiv(tiles, 8) * 8 + 8;
+  const dim3 grid((unsigned)wgs);
+  if (!slots || 2 * tiles > slots) {
+    if (bwd)
+      hipLaunchKernelGGL((experts_gemm_kernel<true, false>), grid, block, 0, stream, p, er, tab, slots);
+    else
+      hipLaunchKernelGGL((experts_gemm_kernel<false, false>), grid, block, 0, stream, p, er, tab, slots);
+  }
+  if (!slots) return;
+  p.piece_out = static_cast<float*>(ws);
+  // at most half the slots in tiles
+  const dim3 pgrid((unsigned)slots);
+  const dim3 rgrid((unsigned)((tiles < slots / 2 ? tiles : slots / 2) * (lg2::BF * lg2::BT / 4 / 256)));
+  if (bwd) {
+    hipLaunchKernelGGL((experts_gemm_kernel<true, true>), pgrid, block, 0, stream, p, er, tab, slots);
+    hipLaunchKernelGGL(experts_pieces_kernel<true>, rgrid, dim3(256), 0, stream, p, er, slots);
+  } else {
+    hipLaunchKernelGGL((experts_gemm_kernel<false, true>), pgrid, block, 0, stream, p, er, tab, slots);
+    hipLaunchKernelGGL(experts_pieces_kernel<false>, rgrid, dim3(256), 0, stream, p, er, slots);
+  }
+}
+
+// s u (or s v) of row `row` (none past `rows`), ranks q .. q + 7, as bf16 hi + lo; the
+// partials are summed in order, and the sum goes to u_out.
+__device__ __forceinline__ void lora_rows(const float* part, int splits, int64_t stride, int64_t row, bool ok, int R,
+                                          int q, float s, float* u_out, u32x4& hi, u32x4& lo) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  const int have = ok ? R - q : 0;
+  const float* src = part + row * R + q;
+  if (have >= 8 && (R & 3) == 0) {
+    for (int k = 0; k < splits; ++k, src += stride) {
+      const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] += a[i];
+        v[i + 4] += b[i];
+      }
     }
+  } else if (have > 0) {
+    for (int k = 0; k < splits; ++k, src += stride) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (i < have) v[i] += src[i];
+    }
+  }
+  if (u_out) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < have) u_out[row * R + q + i] = v[i];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float h0, l0, h1, l1;
+    split_bf16(s * v[2 * i], h0, l0);
+    split_bf16(s * v[2 * i + 1], h1, l1);
+    hi[i] = pack_bf16x2(h0, h1);
+    lo[i] = pack_bf16x2(l0, l1);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// h where experts have few rows: weights straight into MFMA operands
+// ---------------------------------------------------------------------------
+struct StreamArgs {
+  const uint16_t* x;        // M x K
+  const uint8_t* codes;
+  const uint8_t* absmax8;
+  const float* c2;
+  const uint16_t* B;        // E x N x R
+  const float* u;           // usplits x M x R partials of u
+  int usplits;
+  float* u_out;             // M x R or null
+  uint16_t* h;              // M x N
+  float* part;              // ksplits x M x N, used with ksplits > 1
+  int ksplits;
+  int64_t K, N;
+  int R;
+  float s;
+  int groups;               // feature groups
+};
+
+// TB: blocks of 16 rows in a tile.
+template <int TB>
+__global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, ExpertRows er, Nf4Table tab) {
+  constexpr int NW = 4;                  // waves
+  constexpr int NF = 2;                  // blocks of 16 features of a wave
+  constexpr int NS = 2;                  // stages of x in LDS
+  constexpr int ND = 2;                  // pieces of codes in registers
+  constexpr int BT = 16 * TB;
+  constexpr int STAGE = BT * 512;        // 256 k of each row
+  constexpr int XL = TB * 8 / NW;        // 1 KB loads of x per wave and stage
+  constexpr int CL = 4 * NF;             // loads of a piece of codes
+  constexpr int U = NS > ND ? NS : ND;
+  static_assert(U % NS == 0 && U % ND == 0 && TB * 8 % NW == 0, "ring");
+  __shared__ __align__(16) uint8_t s0[STAGE];
+  __shared__ __align__(16) uint8_t s1[STAGE];
+  __shared__ __align__(16) uint8_t s2[NS > 2 ? STAGE : 16];
+  __shared__ __align__(16) uint8_t s3[NS > 3 ? STAGE : 16];
+  uint8_t* const buf4[4] = {s0, s1, s2, s3};
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15;
+  const int g = lane >> 4;
+  // items: expert, feature group, row tile (fastest), so that the tiles that
+  // read the same weights follow each other; a run of them to each XCD
+  int item = 0;
+  Span sp;
+  const bool found = find_span(er, BT, [&](int total) {
+    const int items = total * p.groups;
+    const int run = (items + 7) >> 3;
+    item = ((int)blockIdx.x & 7) * run + ((int)blockIdx.x >> 3);
+    return ((int)blockIdx.x >> 3) < run && item < items ? item / p.groups : -1;
+  }, sp);
+  if (!found) return;
+  const int local = item - (item / p.groups - sp.tile) * p.groups;  // among the expert's items
+  const int fg = local / sp.tiles;
+  const int tile = local % sp.tiles;
+  const int split = (int)blockIdx.y;
+  const int64_t K = p.K;
+  const int pieces = (int)cdiv(K, 256);
+  const int pb = split * pieces / p.ksplits, pe = (split + 1) * pieces / p.ksplits;
+  const int nst = pe - pb;
+  const int t0 = tile * BT;
+  const int nt = (sp.rows - t0 + 15) / 16 < TB ? (sp.rows - t0 + 15) / 16 : TB;  // blocks with rows
+
+  const int64_t cells = p.N * K;
+  const int64_t block0 = sp.e * (cells / kBlock);
+  const uint32_t skew = (uint32_t)(block0 % kGroupBlocks);
+  const uint32_t cbytes = (uint32_t)(cells / 2), abytes = (uint32_t)(cells / kBlock);
+  const uint32_t xbytes = (uint32_t)(sp.rows * K * 2);
+  const brsrc_t rx = make_rsrc(p.x + sp.row0 * K, xbytes);
+  const brsrc_t rc = make_rsrc(p.codes + sp.e * (cells / 2), cbytes);
+  const brsrc_t ra = make_rsrc(p.absmax8 + block0, abytes);
+  const brsrc_t rs = make_rsrc(p.c2 + block0 / kGroupBlocks, (abytes + skew + kGroupBlocks - 1) / kGroupBlocks * 4);
+
+  // x: a 1 KB load holds 2 rows of 256 k.  The 16-byte chunk of k = 64 g + 8 q
+  // sits at 16 (g % 2) + ((8 (g / 2) + q) ^ (t % 16)) of row t: a 16-byte read
+  // serves half of lane group g's rows together with the other half of group
+  // g + 1's, which then take different banks.
+  auto issue_x = [&](int s, uint8_t* stg) {
+#pragma unroll
+    for (int b = 0; b < XL; ++b) {
+      const int blk = wave * XL + b;
+      const int row = 2 * blk + (lane >> 5);
+      const int c = (lane & 31) ^ (row & 15);  // slot -> 16 (g % 2) + 8 (g / 2) + q
+      const int64_t k = (int64_t)(pb + s) * 256 + 64 * ((c >> 4) | ((c >> 2) & 2)) + 8 * (c & 7);
+      dma16(rx, stg + blk * 1024, s < nst && k < K && t0 + row < sp.rows ? (uint32_t)(((t0 + row) * K + k) * 2) : xbytes);
+    }
+  };
+  // codes: a lane takes one 64-weight block of feature row lr for each of the
+  // wave's two 16-feature blocks and piece of 256 k: k = 64 g .. 64 g + 63.
+  // MFMA step q then pairs k = 64 g + 8 q .. + 7 of both operands.
+  const int64_t f0 = (int64_t)fg * (16 * NF * NW) + 16 * NF * wave;
+  const uint32_t cbase = (uint32_t)(((f0 + lr) * K + (int64_t)pb * 256 + 64 * g) / 2);
+  const uint32_t crow = (uint32_t)(16 * K / 2);
+  struct Piece {
+    u32x4 c[NF][2];
+    uint32_t a[NF];
+    float s[NF];
+  };
+  auto load = [&](int s, Piece& P) {
+#pragma unroll
+    for (int b = 0; b < NF; ++b) {
+      const uint32_t off = s < nst ? cbase + b * crow + (uint32_t)s * 128 : cbytes;
+      P.c[b][0] = bload128(rc, off);
+      P.c[b][1] = bload128(rc, off + 16);
+      const uint32_t blk = off / (kBlock / 2);
+      P.a[b] = bload8(ra, blk);
+      P.s[b] = __uint_as_float(bload32(rs, ((blk + skew) >> 8) << 2));
+    }
+  };
+  f32x4 acc[NF][TB];
+#pragma unroll
+  for (int b = 0; b < NF; ++b)
+#pragma unroll
+    for (int t = 0; t < TB; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // the reads of x run one MFMA step ahead
+  auto compute = [&](const uint8_t* stg, const Piece& P) {
+    u32x4 xf[2][TB];
+    auto read = [&](int q) {
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+        xf[q & 1][t] = *reinterpret_cast<const u32x4*>(stg + (16 * t + lr) * 512 + (g & 1) * 256 +
+                                                       (((8 * (g >> 1) + q) ^ lr) << 4));
+    };
+    read(0);
+    MagLut L[NF];
+#pragma unroll
+    for (int b = 0; b < NF; ++b) L[b] = make_mag_lut(tab, e4m3_decode(P.a[b]) * P.s[b]);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      if (q < 7) read(q + 1);
+      if (TB > 1) __builtin_amdgcn_sched_barrier(0);
+      u32x4 w[NF];
+#pragma unroll
+      for (int b = 0; b < NF; ++b) {
+        uint32_t o[4];
+        mag_dequant8(L[b], P.c[b][q >> 2][q & 3], o);
+        w[b] = u32x4{o[0], o[1], o[2], o[3]};
+      }
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int b = 0; b < NF; ++b) acc[b][t] = mfma16x16x32(w[b], xf[q & 1][t], acc[b][t]);
+    }
+  };
+  // Per step: the wave's loads of stage s have landed when no more are in
+  // flight than were issued after them (loads complete in order; the empty
+  // asm keeps the order of issue); the barrier makes that so for all waves,
+  // and frees the stage before.  Steps past the end load nothing.
+  auto fence = []() { asm volatile("" ::: "memory"); };
+  Piece P[ND];
+#pragma unroll
+  for (int j = -(NS > ND ? NS - 1 : ND - 1); j < 0; ++j) {
+    if (j >= -(NS - 1)) issue_x(j + NS - 1, buf4[j + NS - 1]);
+    fence();
+    if (j >= -(ND - 1)) load(j + ND - 1, P[j + ND - 1]);
+    fence();
+  }
+  constexpr int kAfter = (NS - 2) * XL + CL * ((ND < NS ? ND : NS) - 1);
+  auto step = [&](int s, int u) {
+    wait_vmcnt<kAfter>();
+    ring_barrier();
+    issue_x(s + NS - 1, buf4[(u + NS - 1) % NS]);
+    fence();
+    load(s + ND - 1, P[(u + ND - 1) % ND]);
+    fence();
+    compute(buf4[u % NS], P[u % ND]);
+  };
+  const int full = nst - nst % U;
+  for (int sb = 0; sb < full; sb += U) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) step(sb + u, u);
+  }
+#pragma unroll
+  for (int u = 0; u < U - 1; ++u)
+    if (full + u < nst) step(full + u, u);
+  wait_vmcnt<0>();
+
+  // lane holds features f0 + 16 b + 4 g + e of row t0 + 16 t + lr.  The LoRA
+  // term, in the first K split: ranks 32 at a time, s u as bf16 hi + lo.
+  const int R = p.R;
+  if (split == 0) {
+    const uint16_t* B = p.B + sp.e * (p.N * R);
+    for (int q0 = 0; q0 < R; q0 += 32) {
+      u32x4 w[NF];
+#pragma unroll
+      for (int b = 0; b < NF; ++b) {
+        const int64_t f = f0 + 16 * b + lr;
+        const int q = q0 + 8 * g;
+        if (f < p.N && (R & 7) == 0 && q + 8 <= R) {
+          w[b] = *reinterpret_cast<const u32x4*>(B + f * R + q);
+        } else {
+          w[b] = u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (f < p.N && q + i < R) w[b][i >> 1] |= (uint32_t)B[f * R + q + i] << (16 * (i & 1));
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        const int row = t0 + 16 * t + lr;
+        u32x4 hi, lo;
+        lora_rows(p.u, p.usplits, (int64_t)er.M * R, sp.row0 + row, row < sp.rows, R, q0 + 8 * g, p.s,
+                  fg == 0 && wave == 0 ? p.u_out : nullptr, hi, lo);
+#pragma unroll
+        for (int b = 0; b < NF; ++b) {
+          acc[b][t] = mfma16x16x32(w[b], hi, acc[b][t]);
+          acc[b][t] = mfma16x16x32(w[b], lo, acc[b][t]);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+    const int row = t0 + 16 * t + lr;
+    if (row >= sp.rows) continue;
+#pragma unroll
+    for (int b = 0; b < NF; ++b) {
+      const int64_t f = f0 + 16 * b + 4 * g;
+      if (f >= p.N) continue;
+      const f32x4 v = acc[b][t];
+      const int64_t o = (int64_t)(sp.row0 + row) * p.N + f;
+      if (p.ksplits > 1) {
+        float* dst = p.part + (int64_t)split * er.M * p.N + o;
+        if ((p.N & 3) == 0) {
+          *reinterpret_cast<f32x4*>(dst) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (f + e < p.N) dst[e] = v[e];
+        }
+      } else {
+        const u32x2 w = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        if ((p.N & 3) == 0) {
+          *reinterpret_cast<u32x2*>(p.h + o) = w;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (f + e < p.N) p.h[o + e] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+        }
+      }
+    }
+  }
+}
+
+// h = bf16(sum of the K splits, in order), 4 values a thread, for the rows that belong to an
+// expert.
+__global__ __launch_bounds__(256) void experts_stream_sum_kernel(StreamArgs p, ExpertRows er) {
+  int low, top;
+  live_rows(er, low, top);
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int64_t end = (int64_t)top * p.N;
+  if (i + 4 <= (int64_t)low * p.N || i >= end) return;
+  const int64_t stride = (int64_t)er.M * p.N;
+  const int64_t from = (int64_t)low * p.N;
+  if (i >= from && i + 4 <= end && (stride & 3) == 0) {
+    f32x4 v = *reinterpret_cast<const f32x4*>(p.part + i);
+    for (int k = 1; k < p.ksplits; ++k) v += *reinterpret_cast<const f32x4*>(p.part + k * stride + i);
+    *reinterpret_cast<u32x2*>(p.h + i) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     return;
   }
-  const dim3 grid((unsigned)(cdiv(tiles, 8) * 8));
-  if (bwd)
-    hipLaunchKernelGGL((experts_gemm_kernel<true, false>), grid, block, 0, stream, p, er, tab);
+  for (int e = 0; e < 4; ++e) {
+    if (i + e < from || i + e >= end) continue;
+    float v = p.part[i + e];
+    for (int k = 1; k < p.ksplits; ++k) v += p.part[k * stride + i + e];
+    p.h[i + e] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+  }
+}
+
+struct StreamPlan {
+  int tb;       // 16-row blocks of a tile, 0: the GEMM takes the call
+  int groups;   // of 128 features
+  int ksplits;
+};
+
+constexpr int kStreamWaves = 4;
+
+static StreamPlan stream_plan(int64_t M, int64_t E, int64_t N, int64_t K) {
+  const int64_t rows = cdiv(M, E < M ? E : M);  // of an expert, if all have as many
+  StreamPlan s{};
+  s.tb = rows <= 16 ? 1 : rows <= 32 ? 2 : 0;
+  s.ksplits = 1;
+  if (!s.tb) return s;
+  s.groups = (int)cdiv(N, 32 * kStreamWaves);
+  const int64_t items = most_tiles(M, E, 16 * s.tb) * s.groups;
+  int64_t ks = 4 * (int64_t)device_cus() / items;
+  const int64_t most = cdiv(K, 256) / 2;
+  ks = ks > most ? most : ks;
+  ks = ks > 8 ? 8 : ks;
+  s.ksplits = ks < 1 ? 1 : (int)ks;
+  return s;
+}
+
+size_t experts_stream_ws_bytes(int64_t M, int64_t E, int64_t N, int64_t K) {
+  const StreamPlan s = stream_plan(M, E, N, K);
+  return s.tb && s.ksplits > 1 ? (size_t)s.ksplits * M * N * sizeof(float) : 0;
+}
+bool experts_stream_takes(int64_t M, int64_t E, int64_t N, int64_t K) { return stream_plan(M, E, N, K).tb != 0; }
+
+void launch_experts_stream(const int32_t* offsets, int64_t E, const uint16_t* x, const uint8_t* codes,
+                           const uint8_t* absmax8, const float* c2, const uint16_t* B, const float* u, int usplits,
+                           float* u_out, uint16_t* h, int64_t M, int64_t n, int64_t m, int r, float s, void* ws,
+                           const Nf4Table& tab, hipStream_t stream) {
+  const StreamPlan plan = stream_plan(M, E, m, n);
+  StreamArgs p{x, codes, absmax8, c2, B, u, usplits, u_out, h, static_cast<float*>(ws), plan.ksplits, n, m, r, s, plan.groups};
+  const ExpertRows er{offsets, (int)E, (int)M};
+  const int64_t items = most_tiles(M, E, 16 * plan.tb) * plan.groups;
+  const dim3 grid((unsigned)(cdiv(items, 8) * 8), (unsigned)plan.ksplits), block(64 * kStreamWaves);
+  if (plan.tb == 1)
+    hipLaunchKernelGGL((experts_stream_kernel<1>), grid, block, 0, stream, p, er, tab);
   else
-    hipLaunchKernelGGL((experts_gemm_kernel<false, false>), grid, block, 0, stream, p, er, tab);
+    hipLaunchKernelGGL((experts_stream_kernel<2>), grid, block, 0, stream, p, er, tab);
+  if (plan.ksplits > 1)
+    hipLaunchKernelGGL(experts_stream_sum_kernel, dim3((unsigned)cdiv(M * m, 1024)), dim3(256), 0, stream, p, er);
 }
 
 // ---------------------------------------------------------------------------
@@ -369,19 +837,9 @@ __global__ __launch_bounds__(256) void experts_factor_kernel(FactorJob a, Factor
   const int i = (int)(blockIdx.x * 256 + threadIdx.x);  // rank pairs of all rows (fewer than 2^29)
   const int row = i / (RP / 2);
   const int q = i % (RP / 2) * 2;
-  // the rows that belong to an expert: offsets[0] .. the largest offset
-  int top = 0;
-  for (int e = threadIdx.x & 63; e <= er.E; e += 64) {
-    const int o = er.offsets[e];
-    top = o > top ? o : top;
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    const int o = __shfl_xor(top, d, 64);
-    top = o > top ? o : top;
-  }
-  const int low = er.offsets[0];
-  if (row >= er.M || row < low || row >= top) return;
+  int low, top;
+  live_rows(er, low, top);
+  if (row < low || row >= top) return;
   float v[2] = {0.0f, 0.0f};
   const int64_t stride = (int64_t)er.M * R;
   const float* src = j.part + (int64_t)row * R + q;

@@ -324,15 +324,25 @@ __device__ __forceinline__ void gemm_producer(const GemmArgs& p, const Nf4Table&
   }
 }
 
-// MFMA waves (512 threads): each owns a WF-feature x WT-token output tile,
-// 128 x 64 in the forward and 64 x 128 in the backward, where the W'
-// fragments come from half-rate transposed reads and the activation
-// fragments from full-rate ones (the 64 x 128 shape halves the former).
-template <bool kBwd, bool kPieces, bool kSkip>
+// Features and tokens of one MFMA wave's part of a tile of `rows` tokens.
+// Whole tiles: 128 x 64 in the forward and 64 x 128 in the backward, where the
+// W' fragments come from half-rate transposed reads and the activation
+// fragments from full-rate ones (the 64 x 128 shape halves the former).  Tiles
+// of at most 128 or 64 tokens (experts' ragged last ones): all eight waves
+// share what there is.
+template <bool kBwd, int kRows>
+struct WaveTile {
+  static constexpr int F = kRows == 64 ? 32 : kRows == 128 ? 64 : kBwd ? 64 : 128;
+  static constexpr int T = 256 * kRows / 8 / F;
+};
+
+// MFMA waves (512 threads): each owns a WF-feature x WT-token output tile.
+// kRows: tokens that the tile covers at most, 256, 128 or 64.
+template <bool kBwd, bool kPieces, bool kSkip, int kRows = lg2::BT>
 __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds& lds, int tid, int64_t f0,
                                               int64_t t0, int k0, int nk, bool lora, int split, uint32_t* lds_word) {
-  constexpr int WF = kBwd ? 64 : 128;
-  constexpr int WT = 128 * 64 / WF;
+  constexpr int WF = WaveTile<kBwd, kRows>::F;
+  constexpr int WT = WaveTile<kBwd, kRows>::T;
   constexpr int NI = WF / 16;  // 16-feature fragments
   constexpr int NJ = WT / 16;  // 16-token fragments
   const int lane = tid & 63;
@@ -356,18 +366,19 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
   using T = lg2::Tile<kBwd>;
-  // Activation tile copy: this wave fills rows 32 w .. 32 w + 31 of the tile,
+  // Activation tile copy: this wave fills an eighth of the tile's rows (32 of 256),
   // 8 rows (1 KB) per load; lane l lands at byte 16 l of its block, i.e. row
   // l / 8, chunk position l % 8, which holds chunk (l % 8) ^ (l / 8).  Rows
   // past M are out of the buffer's range and read 0.
   const brsrc_t r_act = make_rsrc(p.act, (uint32_t)(p.M * p.K * 2));
-  uint32_t act_off = (uint32_t)(((t0 + 32 * wave + (lane >> 3)) * p.K + 8 * ((lane & 7) ^ (lane >> 3)) +
+  constexpr int kCopies = kRows / 64;  // 8-row loads of a wave
+  uint32_t act_off = (uint32_t)(((t0 + 8 * kCopies * wave + (lane >> 3)) * p.K + 8 * ((lane & 7) ^ (lane >> 3)) +
                                   (int64_t)k0 * lg2::BK) * 2);
   const uint32_t act_blk = (uint32_t)(8 * p.K * 2);
   auto copy_act = [&](uint8_t* tile) {
-    uint8_t* dst = tile + 32 * 128 * wave;
+    uint8_t* dst = tile + 8 * kCopies * 128 * wave;
 #pragma unroll
-    for (int b = 0; b < 4; ++b)
+    for (int b = 0; b < kCopies; ++b)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (__attribute__((address_space(3))) void*)(dst + 1024 * b), 16,
                                                act_off + act_blk * b, 0, 0, 0);
     act_off += lg2::BK * 2;
@@ -402,7 +413,18 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
   // larger one software-pipelined one ahead; the scheduling barriers keep the
   // compiler from hoisting all of it (the accumulators leave room for two).
   auto mfma_step = [&](const uint8_t* sW, const uint8_t* sA, int kk) {
-    if constexpr (NI >= NJ) {
+    if constexpr (kRows < lg2::BT) {
+      // few accumulators: all fragments at once
+      u32x4 a[NI], b[NJ];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) a[i] = load_a(sW, kk, i);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) b[j] = load_b(sA, kk, j);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i][j] = mfma16x16x32(a[i], b[j], acc[i][j]);
+    } else if constexpr (NI >= NJ) {
       u32x4 b[NJ];
 #pragma unroll
       for (int j = 0; j < NJ; ++j) b[j] = load_b(sA, kk, j);
@@ -548,11 +570,13 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
   // The K loop's last barrier has freed all tiles.  Each wave stages its
   // WT x WF tile as [WT rows][2 WF bytes] in 16 KB of its own (waves 2w',
   // 2w' + 1 share one 32 KB tile array).  The 16-byte chunk c of row t sits at
-  // position c ^ (t % 16) for 256-byte rows and c ^ ((t / 2) % 8) for 128-byte
-  // rows, so the 8-byte writes (16 rows x 4 lanes) and the 16-byte row reads
+  // position c ^ (t % 16) for 256-byte rows, c ^ ((t / 2) % 8) for 128-byte
+  // rows and c ^ ((t / 4) % 4) for 64-byte rows, so the 8-byte writes (16 rows x 4 lanes) and the 16-byte row reads
   // are free of bank conflicts.
   constexpr int CPR = WF / 8;  // 16-byte chunks per staged row
-  auto spos = [](int row, int c) { return CPR == 16 ? (c ^ (row & 15)) : (c ^ ((row >> 1) & 7)); };
+  auto spos = [](int row, int c) {
+    return CPR == 16 ? (c ^ (row & 15)) : CPR == 8 ? (c ^ ((row >> 1) & 7)) : (c ^ ((row >> 2) & 3));
+  };
   uint8_t* stg = ((wave >> 1) == 0 ? lds.a[0] : (wave >> 1) == 1 ? lds.a[1] : (wave >> 1) == 2 ? lds.w[0] : lds.w[1]) +
                  16384 * (wave & 1);
 #pragma unroll

@@ -624,7 +624,9 @@ qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
  * fp32(largest root / 255^2); a value that is not 0 takes k >= 1.  Each value
  * takes the nearest of them, of two as near the lower, decided in 64 bits; a d
  * below 2^-126 is 0, and all of its block.
- * Every pointer 16-byte aligned; tensors must not overlap.
+ * Every pointer 16-byte aligned, but for the steps, which are read one by one
+ * (4 bytes: the tensors may be slices of one storage, each from a block's
+ * border on); tensors must not overlap.
  */
 typedef struct {
   int64_t count;
@@ -680,7 +682,7 @@ qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, doubl
 
 /*
  * The fp32 values that an 8-bit moment's `count` codes stand for; second: 0
- * for an exp_avg, 1 for an exp_avg_sq.
+ * for an exp_avg, 1 for an exp_avg_sq.  steps: 4-byte aligned.
  */
 qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* codes, const float* steps, float* out,
                                   qlora_stream_t stream);

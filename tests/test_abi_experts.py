@@ -10,6 +10,7 @@ import torch
 
 P = ctypes.c_void_p(1 << 20)   # non-NULL and aligned; never dereferenced on error paths
 MIS = ctypes.c_void_p((1 << 20) + 4)
+ODD = ctypes.c_void_p((1 << 20) + 2)
 NAN, INF = float("nan"), float("inf")
 
 
@@ -75,7 +76,7 @@ def tensor(_lib, count=100, p=P, p16=P, g=P, m=P, v=P, md=P, vd=P, gt=0, mom=1):
 BAD = [(dict(count=0), -2), (dict(count=-1), -2), (dict(count=1 << 40), -2), (dict(gt=2), -7), (dict(gt=-1), -7),
        (dict(mom=2), -7), (dict(mom=-1), -7), (dict(p=None), -1), (dict(g=None), -1), (dict(m=None), -1),
        (dict(v=None), -1), (dict(md=None), -1), (dict(vd=None), -1), (dict(p=MIS), -4), (dict(p16=MIS), -4),
-       (dict(g=MIS), -4), (dict(m=MIS), -4), (dict(v=MIS), -4), (dict(md=MIS), -4), (dict(vd=MIS), -4)]
+       (dict(g=MIS), -4), (dict(m=MIS), -4), (dict(v=MIS), -4), (dict(md=ODD), -4), (dict(vd=ODD), -4)]
 
 
 def test_adamw_plan(lib):
@@ -135,7 +136,7 @@ def test_moment8_values(lib):
     assert f(0, 0, P, P, P, None) == -2 and f(0, 1 << 40, P, P, P, None) == -2
     for i in range(3):
         assert f(0, 8, *[None if j == i else P for j in range(3)], None) == -1
-        assert f(1, 8, *[MIS if j == i else P for j in range(3)], None) == -4
+        assert f(1, 8, *[(ODD if i == 1 else MIS) if j == i else P for j in range(3)], None) == -4
 
 
 def test_binding_refuses_host_tensors_and_wrong_moments():
