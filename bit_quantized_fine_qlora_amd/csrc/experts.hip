@@ -40,23 +40,27 @@ struct Span {
   int slot;   // tiles before this one that belong to experts with more than one
 };
 
-__device__ __forceinline__ int wave_scan_max(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d, 64);
-    v = lane >= d && o > v ? o : v;
-  }
+// Inclusive scans over the wave's lanes of values that are not negative, by
+// DPP row shifts and broadcasts (lanes without a source get 0).
+template <typename Op>
+__device__ __forceinline__ int wave_scan(int v, Op op) {
+  auto step = [&](auto ctrl, auto rows) {
+    v = op(v, __builtin_amdgcn_update_dpp(0, v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false));
+  };
+  using std::integral_constant;
+  step(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});  // row_shr:1
+  step(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});  // row_shr:2
+  step(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});  // row_shr:4
+  step(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});  // row_shr:8
+  step(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast:15 into rows 1 and 3
+  step(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast:31 into rows 2 and 3
   return v;
 }
+__device__ __forceinline__ int wave_scan_max(int v) {
+  return wave_scan(v, [](int a, int b) { return a > b ? a : b; });
+}
 __device__ __forceinline__ int wave_scan_add(int v) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_up(v, d, 64);
-    v += lane >= d ? o : 0;
-  }
-  return v;
+  return wave_scan(v, [](int a, int b) { return a + b; });
 }
 
 // 64 experts at a time, one a lane.  Offsets are held within 0 .. M and below
@@ -78,8 +82,7 @@ struct ExpertScan {
     const int e = first + lane;
     int last = held(r.offsets[e < r.E ? e + 1 : r.E], r.M);
     last = wave_scan_max(last > end ? last : end);
-    const int prev = __shfl_up(last, 1, 64);
-    row0 = lane ? prev : end;
+    row0 = __builtin_amdgcn_update_dpp(end, last, 0x138, 0xF, 0xF, false);  // wave_shr:1, `end` into lane 0
     rows = e < r.E ? last - row0 : 0;
     t = (rows + bt - 1) / bt;
     t_incl = wave_scan_add(t);
@@ -781,10 +784,11 @@ static inline int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 6
 
 int experts_down_splits(int64_t M, int64_t E, int64_t K, int R) {
   const int64_t slots = (int64_t)(rank_blocks(R) <= 4 ? 2 : 1) * device_cus();
-  int64_t want = cdiv(slots, most_tiles(M, E, sk::DT));
+  int64_t want = slots / most_tiles(M, E, sk::DT);  // one round
   const int64_t most = cdiv(K, 512);
   if (want > most) want = most;
   if (want > 64) want = 64;
+  if (want < 1) want = 1;
   return (int)cdiv(K, cdiv(cdiv(K, want), 128) * 128);
 }
 
@@ -919,9 +923,10 @@ __device__ __forceinline__ int plane_row(int t) {
   return RB == 1 ? t ^ (((t >> 3) & 1) << 2) : t;
 }
 
-template <int RB, int NS>
-__global__ __launch_bounds__(256) void experts_token_kernel(TokenArgs a) {
-  constexpr int XB = sk::TS * 256;       // 64 rows x 128 columns
+template <int RB, int NS, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void experts_token_kernel(TokenArgs a) {
+  constexpr int ROW = 64 * WAVES;        // bytes of a row of the stage: 32 columns a wave
+  constexpr int XB = sk::TS * ROW;       // 64 rows
   constexpr int PB = sk::TS * 32 * RB;   // one plane: 64 rows x 16 RB ranks
   constexpr int STAGE = XB + 2 * PB;
   __shared__ __align__(16) uint8_t s0[STAGE];
@@ -944,7 +949,7 @@ __global__ __launch_bounds__(256) void experts_token_kernel(TokenArgs a) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15;
   const int lq = lane >> 4;
-  const int64_t j0 = (int64_t)(bid % job.tiles) * sk::TJ;
+  const int64_t j0 = (int64_t)(bid % job.tiles) * (32 * WAVES);
   const int tbeg = sp.tile * job.chunk;
   const int tend = tbeg + job.chunk < sp.rows ? tbeg + job.chunk : sp.rows;
   const int nst = (tend - tbeg + sk::TS - 1) / sk::TS;
@@ -954,23 +959,26 @@ __global__ __launch_bounds__(256) void experts_token_kernel(TokenArgs a) {
   const uint32_t pbytes = plane + (uint32_t)sp.rows * (32u * RB);
   const brsrc_t rx = make_rsrc(job.X + sp.row0 * ld, xbytes);
   const brsrc_t rp = make_rsrc(job.P + (int64_t)sp.row0 * (16 * RB), pbytes);
-  const int xrow = lane >> 4;
-  const int slot = lane & 15;
-  constexpr int LMIN = 4 + RB;
+  constexpr int XR = 16 / WAVES;         // rows of a 1 KB load
+  const int xrow = lane / (4 * WAVES);
+  const int slot = lane % (4 * WAVES);
+  static_assert(4 * RB % WAVES == 0, "blocks of the planes");
+  constexpr int PL = 4 * RB / WAVES;     // loads of the planes per wave
+  constexpr int LMIN = 4 + PL;
   auto issue = [&](int s, uint8_t* stg) {
     const int tb = tbeg + s * sk::TS;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {  // rows 16 w .. 16 w + 15 of the stage, 4 a load (swtg)
+    for (int b = 0; b < 4; ++b) {  // XR rows a load; 32-byte unit u of a row at u ^ f, as in swtg
       const int blk = 4 * wave + b;
-      const int row = 4 * blk + xrow;
+      const int row = XR * blk + xrow;
       const int f = (row & 3) | (((row >> 3) & 1) << 2);
       const int c = ((((slot >> 1) ^ f)) << 1) | (slot & 1);
       const int64_t j = j0 + 8 * c;
       dma16(rx, stg + blk * 1024, (tb + row < tend && j < ld) ? (uint32_t)(((tb + row) * ld + j) * 2) : xbytes);
     }
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {  // 1 KB blocks 4 b + w of the two planes (2 RB blocks each)
-      const int id = 4 * b + wave;
+    for (int b = 0; b < PL; ++b) {  // 1 KB blocks of the two planes (2 RB blocks each)
+      const int id = WAVES * b + wave;
       const int pl = id / (2 * RB);
       const int pos = (id % (2 * RB)) * 64 + lane;  // 16-byte piece of the plane's tile
       const int row = plane_row<RB>(pos / (2 * RB));
@@ -991,6 +999,10 @@ __global__ __launch_bounds__(256) void experts_token_kernel(TokenArgs a) {
     const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p1));
     return u32x4{lo[0], lo[1], hi[0], hi[1]};
   };
+  auto xat = [](int t, int c) -> uint32_t {
+    const int f = (t & 3) | (((t >> 3) & 1) << 2);
+    return (uint32_t)(t * ROW + (((c >> 1) ^ f) << 5) + ((c & 1) << 4));
+  };
   auto compute = [&](const uint8_t* stg) {
 #pragma unroll
     for (int kk = 0; kk < 2; ++kk) {
@@ -1000,7 +1012,7 @@ __global__ __launch_bounds__(256) void experts_token_kernel(TokenArgs a) {
 #pragma unroll
       for (int ib = 0; ib < 2; ++ib) {
         const int c = 2 * (2 * wave + ib) + (tr_c >> 1);
-        x[ib] = read_tr(stg + swtg(t, c) + (tr_c & 1) * 8, stg + swtg(t + 4, c) + (tr_c & 1) * 8);
+        x[ib] = read_tr(stg + xat(t, c) + (tr_c & 1) * 8, stg + xat(t + 4, c) + (tr_c & 1) * 8);
       }
 #pragma unroll
       for (int cb = 0; cb < RB; ++cb) {
@@ -1051,37 +1063,50 @@ __global__ __launch_bounds__(256) void experts_token_kernel(TokenArgs a) {
   }
 }
 
-constexpr int kSumCells = 4096;  // of a workgroup
+constexpr int kSumCells = 1024;  // of a workgroup, 4 a thread
 
 __global__ __launch_bounds__(256) void experts_sum_kernel(TokenArgs a) {
   const TokenJob& job = a.job[blockIdx.z];
   const int64_t cells = job.J * a.R;
-  const int64_t i0 = (int64_t)blockIdx.x * kSumCells;
-  if (i0 >= cells) return;
+  const int64_t i = (int64_t)blockIdx.x * kSumCells + 4 * (int)threadIdx.x;
+  if ((int64_t)blockIdx.x * kSumCells >= cells) return;
   const Span sp = expert_span(a.er, job.chunk, (int)blockIdx.y);
-  if (sp.tiles == 1) return;
-  uint16_t* out = job.out + sp.e * cells;
-  const float* part = job.part + sp.slot * cells;
-  const int64_t i1 = i0 + kSumCells < cells ? i0 + kSumCells : cells;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += 256) {
-    float s = 0.0f;
-    for (int k = 0; k < sp.tiles; k += 8) {
-      float w[8];
+  if (sp.tiles == 1 || i >= cells) return;
+  uint16_t* out = job.out + sp.e * cells + i;
+  const float* part = job.part + sp.slot * cells + i;
+  if ((cells & 3) == 0) {
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < sp.tiles; k += 4) {
+      f32x4 w[4];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) w[x] = k + x < sp.tiles ? part[(k + x) * cells + i] : 0.0f;
+      for (int x = 0; x < 4; ++x)  // the loads go out together; what is past the end is loaded again and not added
+        w[x] = *reinterpret_cast<const f32x4*>(part + (k + x < sp.tiles ? k + x : k) * cells);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) s += w[x];
+      for (int x = 0; x < 4; ++x)
+        if (k + x < sp.tiles) s += w[x];
     }
-    out[i] = (uint16_t)(pack_bf16x2(a.s * s, 0.0f) & 0xFFFFu);
+    *reinterpret_cast<u32x2*>(out) =
+        u32x2{pack_bf16x2(a.s * s[0], a.s * s[1]), pack_bf16x2(a.s * s[2], a.s * s[3])};
+    return;
+  }
+  for (int e = 0; e < 4 && i + e < cells; ++e) {
+    float s = 0.0f;
+    for (int k = 0; k < sp.tiles; ++k) s += part[k * cells + e];
+    out[e] = (uint16_t)(pack_bf16x2(a.s * s, 0.0f) & 0xFFFFu);
   }
 }
 
-// Rows of a chunk: enough workgroups for a few rounds of the chip (rows of
-// experts differ, so one round would end with the longest), but no fewer than
-// 256 rows, below which the sums weigh as much as the rows.
+// Waves of a workgroup, 32 columns each: at 64 ranks, where the planes of a
+// stage are as large as 128 columns of it, 8.
+static int token_waves(int R) { return rank_blocks(R) == 4 ? 8 : 4; }
+
+// Rows of a chunk: as many workgroups as run at once, if all experts had
+// whole chunks, but no fewer than 256 rows, below which the sums weigh as much
+// as the rows (4 x 8192 x 28672, 4096 rows, 64 ranks: 72 us and 10 us for the
+// sums; with chunks of a third 91 and 19 us).
 static int token_chunk(int64_t M, int64_t J, int R) {
-  const int64_t want = (int64_t)3 * (rank_blocks(R) <= 2 ? 2 : 1) * device_cus();
-  int64_t c = cdiv(cdiv(M * cdiv(J, sk::TJ), want), 64) * 64;
+  const int64_t want = (int64_t)(rank_blocks(R) <= 2 ? 2 : 1) * device_cus();
+  const int64_t c = cdiv(cdiv(M * cdiv(J, 32 * token_waves(R)), want), 64) * 64;
   return (int)(c < 256 ? 256 : c);
 }
 
@@ -1090,25 +1115,26 @@ size_t experts_token_ws_bytes(int64_t M, int64_t J, int R) {
   return (size_t)(2 * M / token_chunk(M, J, R)) * J * R * sizeof(float);
 }
 
-bool experts_token_fits(int64_t M, int64_t E, int64_t J) { return most_tiles(M, E, 256) * cdiv(J, sk::TJ) < ((int64_t)1 << 30); }
+bool experts_token_fits(int64_t M, int64_t E, int64_t J) { return most_tiles(M, E, 256) * cdiv(J, 128) < ((int64_t)1 << 30); }
 
 void launch_experts_token(const uint16_t* x, const uint16_t* vplanes, uint16_t* grad_A, float* part_a,
                           const uint16_t* g, int64_t g_ld, const uint16_t* uplanes, uint16_t* grad_B, float* part_b,
                           const int32_t* offsets, int64_t M, int64_t E, int64_t n, int64_t m, int R, float s,
                           hipStream_t stream) {
   TokenArgs a{};
-  a.job[0] = TokenJob{x, n, n, vplanes, grad_A, part_a, (int)cdiv(n, sk::TJ), token_chunk(M, n, R), true};
-  a.job[1] = TokenJob{g, m, g_ld, uplanes, grad_B, part_b, (int)cdiv(m, sk::TJ), token_chunk(M, m, R), false};
+  const int tj = 32 * token_waves(R);
+  a.job[0] = TokenJob{x, n, n, vplanes, grad_A, part_a, (int)cdiv(n, tj), token_chunk(M, n, R), true};
+  a.job[1] = TokenJob{g, m, g_ld, uplanes, grad_B, part_b, (int)cdiv(m, tj), token_chunk(M, m, R), false};
   a.er = ExpertRows{offsets, (int)E, (int)M};
   a.R = R;
   a.s = s;
   a.first = (int)(most_tiles(M, E, a.job[0].chunk) * a.job[0].tiles);
   const dim3 grid((unsigned)(a.first + most_tiles(M, E, a.job[1].chunk) * a.job[1].tiles));
   switch (rank_blocks(R)) {
-    case 1: hipLaunchKernelGGL((experts_token_kernel<1, 3>), grid, dim3(256), 0, stream, a); break;
-    case 2: hipLaunchKernelGGL((experts_token_kernel<2, 3>), grid, dim3(256), 0, stream, a); break;
-    case 4: hipLaunchKernelGGL((experts_token_kernel<4, 4>), grid, dim3(256), 0, stream, a); break;
-    default: hipLaunchKernelGGL((experts_token_kernel<8, 3>), grid, dim3(256), 0, stream, a); break;
+    case 1: hipLaunchKernelGGL((experts_token_kernel<1, 3, 4>), grid, dim3(256), 0, stream, a); break;
+    case 2: hipLaunchKernelGGL((experts_token_kernel<2, 3, 4>), grid, dim3(256), 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((experts_token_kernel<4, 3, 8>), grid, dim3(512), 0, stream, a); break;
+    default: hipLaunchKernelGGL((experts_token_kernel<8, 3, 4>), grid, dim3(256), 0, stream, a); break;
   }
   const int64_t most = (n > m ? n : m) * R;
   hipLaunchKernelGGL(experts_sum_kernel, dim3((unsigned)cdiv(most, kSumCells), (unsigned)E, 2), dim3(256), 0, stream,
