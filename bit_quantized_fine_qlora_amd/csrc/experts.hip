@@ -293,10 +293,10 @@ __global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p,
   const int64_t left = p.M - t0;
   if (tid >= 64 * lg2::kMfmaWaves)
     gemm_producer<kBwd>(p, tab, lds, tid - 64 * lg2::kMfmaWaves, f0, t0, k0, ks, lora, 0, &lds_word, skew);
-  else if (left >= lg2::BT)
+  else if (left > 192)
     gemm_consumer<kBwd, kPieces, false>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else if (left > 128)
-    gemm_consumer<kBwd, kPieces, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 192>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else if (left > 64)
     gemm_consumer<kBwd, kPieces, false, 128>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else
@@ -345,8 +345,10 @@ __global__ __launch_bounds__(256) void experts_pieces_kernel(GemmArgs p, ExpertR
   if (!found) return;
   p.pieces = __builtin_amdgcn_readfirstlane(pieces);
   const int left = s.rows - s.tile * lg2::BT;
-  if (left > 128)
+  if (left > 192)
     experts_pieces_tile<kBwd, 256>(p, s, tile, rem);
+  else if (left > 128)
+    experts_pieces_tile<kBwd, 192>(p, s, tile, rem);
   else if (left > 64)
     experts_pieces_tile<kBwd, 128>(p, s, tile, rem);
   else

@@ -328,16 +328,16 @@ __device__ __forceinline__ void gemm_producer(const GemmArgs& p, const Nf4Table&
 // Whole tiles: 128 x 64 in the forward and 64 x 128 in the backward, where the
 // W' fragments come from half-rate transposed reads and the activation
 // fragments from full-rate ones (the 64 x 128 shape halves the former).  Tiles
-// of at most 128 or 64 tokens (experts' ragged last ones): all eight waves
+// of at most 192, 128 or 64 tokens (experts' ragged last ones): all eight waves
 // share what there is.
 template <bool kBwd, int kRows>
 struct WaveTile {
-  static constexpr int F = kRows == 64 ? 32 : kRows == 128 ? 64 : kBwd ? 64 : 128;
+  static constexpr int F = kRows == 64 ? 32 : kRows < 256 ? 64 : kBwd ? 64 : 128;
   static constexpr int T = 256 * kRows / 8 / F;
 };
 
 // MFMA waves (512 threads): each owns a WF-feature x WT-token output tile.
-// kRows: tokens that the tile covers at most, 256, 128 or 64.
+// kRows: tokens that the tile covers at most, 256, 192, 128 or 64.
 template <bool kBwd, bool kPieces, bool kSkip, int kRows = lg2::BT>
 __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds& lds, int tid, int64_t f0,
                                               int64_t t0, int k0, int nk, bool lora, int split, uint32_t* lds_word) {
