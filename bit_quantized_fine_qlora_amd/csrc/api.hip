@@ -1243,24 +1243,20 @@ qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
   if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
   float* const v = at<float>(workspace, w.v);
-  const uint16_t* gk = g;
-  if (w.m_pad != m) {
+  const bool direct = experts_b_direct(r), whole = w.m_pad == m;
+  uint16_t* const gp = whole ? nullptr : at<uint16_t>(workspace, w.gpad);
+  uint16_t* const bt = direct ? nullptr : at<uint16_t>(workspace, w.Bt);
+  if (gp || bt) {
     Timed tm("transpose", hs);
-    uint16_t* const gp = at<uint16_t>(workspace, w.gpad);
-    launch_pad_cols_bf16(g, M, m, w.m_pad, gp, hs);
-    gk = gp;
+    launch_experts_prepare(g, gp, B, bt, M, E, m, r, w.m_pad, hs);
   }
-  const bool direct = experts_b_direct(r);
-  if (!direct) {
-    Timed tm("transpose", hs);
-    launch_experts_transpose(B, E, m, r, w.m_pad, at<uint16_t>(workspace, w.Bt), hs);
-  }
+  const uint16_t* const gk = whole ? g : gp;
   uint16_t* const vplanes = at<uint16_t>(workspace, w.vplanes);
   uint16_t* const uplanes = at<uint16_t>(workspace, w.uplanes);
   {
     Timed tm("experts_down", hs);
     float* const part = at<float>(workspace, w.part);
-    launch_experts_down(gk, offsets, M, E, w.m_pad, direct ? B : at<uint16_t>(workspace, w.Bt), direct,
+    launch_experts_down(gk, offsets, M, E, w.m_pad, direct ? B : bt, direct,
                         direct ? m : w.m_pad, r, part, w.splits, hs);
     FactorJob jobs[2] = {{part, w.splits, grad_x ? v : nullptr, vplanes}, {u, 1, nullptr, uplanes}};
     if (!u) {

@@ -29,8 +29,8 @@ void launch_experts_stream(const int32_t* offsets, int64_t E, const uint16_t* x,
 int experts_down_splits(int64_t M, int64_t E, int64_t K, int R);
 void launch_experts_down(const uint16_t* X, const int32_t* offsets, int64_t M, int64_t E, int64_t K, const uint16_t* Y,
                          bool yt, int64_t yrows, int R, float* part, int splits, hipStream_t stream);
-void launch_experts_transpose(const uint16_t* B, int64_t E, int64_t m, int R, int64_t ld, uint16_t* out,
-                              hipStream_t stream);
+void launch_experts_prepare(const uint16_t* g, uint16_t* gout, const uint16_t* B, uint16_t* bout, int64_t M, int64_t E,
+                            int64_t m, int R, int64_t ld, hipStream_t stream);
 size_t experts_planes_bytes(int64_t M, int R);
 void launch_experts_factor(const FactorJob* jobs, int count, const int32_t* offsets, int64_t M, int64_t E, int R,
                            hipStream_t stream);

@@ -816,23 +816,36 @@ void launch_experts_down(const uint16_t* X, const int32_t* offsets, int64_t M, i
   }
 }
 
-// B_e^T (R x ld, zeros from column m on) of every expert, for ranks whose rows
-// of B are not whole 16-byte pieces.
-__global__ __launch_bounds__(256) void experts_transpose_kernel(const uint16_t* __restrict__ B, int64_t m, int R,
-                                                                int64_t ld, int64_t count,
-                                                                uint16_t* __restrict__ out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // over E x R x ld
-  if (i >= count) return;
-  const int64_t f = i % ld, eq = i / ld;
-  const int64_t e = eq / R, q = eq % R;
-  out[i] = f < m ? B[(e * m + f) * R + q] : (uint16_t)0;
+// What the kernels cannot read as it stands, in one launch: rows of g whose
+// length is not a multiple of 8, copied to rows of ld = m rounded up to 64 with
+// zeros behind; and B_e^T (R x ld, zeros from column m on) of every expert, for
+// ranks whose rows of B are not whole 16-byte pieces.  Either may be null.
+__global__ __launch_bounds__(256) void experts_prepare_kernel(const uint16_t* __restrict__ g, int64_t gcount,
+                                                              uint16_t* __restrict__ gout,
+                                                              const uint16_t* __restrict__ B, int64_t bcount,
+                                                              uint16_t* __restrict__ bout, int64_t m, int R,
+                                                              int64_t ld, int64_t gblocks) {
+  if ((int64_t)blockIdx.x < gblocks) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;  // over M x ld
+    if (i >= gcount) return;
+    const int64_t t = i / ld, f = i % ld;
+    gout[i] = f < m ? g[t * m + f] : (uint16_t)0;
+  } else {
+    const int64_t i = ((int64_t)blockIdx.x - gblocks) * 256 + threadIdx.x;  // over E x R x ld
+    if (i >= bcount) return;
+    const int64_t f = i % ld, eq = i / ld;
+    const int64_t e = eq / R, q = eq % R;
+    bout[i] = f < m ? B[(e * m + f) * R + q] : (uint16_t)0;
+  }
 }
 
-void launch_experts_transpose(const uint16_t* B, int64_t E, int64_t m, int R, int64_t ld, uint16_t* out,
-                              hipStream_t stream) {
-  const int64_t count = E * R * ld;
-  hipLaunchKernelGGL(experts_transpose_kernel, dim3((unsigned)cdiv(count, 256)), dim3(256), 0, stream, B, m, R, ld,
-                     count, out);
+void launch_experts_prepare(const uint16_t* g, uint16_t* gout, const uint16_t* B, uint16_t* bout, int64_t M, int64_t E,
+                            int64_t m, int R, int64_t ld, hipStream_t stream) {
+  const int64_t gcount = gout ? M * ld : 0, bcount = bout ? E * R * ld : 0;
+  const int64_t gblocks = cdiv(gcount, 256), blocks = gblocks + cdiv(bcount, 256);
+  if (blocks)
+    hipLaunchKernelGGL(experts_prepare_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, g, gcount, gout, B, bcount,
+                       bout, m, R, ld, gblocks);
 }
 
 // Sums the splits of u or v in order: fp32 out (may be null) and, for the
@@ -891,7 +904,8 @@ void launch_experts_factor(const FactorJob* jobs, int count, const int32_t* offs
 // their own layout and both planes of the factor, read transposed as MFMA
 // operands.  An expert whose rows are one chunk gets its gradient from here;
 // of more chunks each leaves fp32 sums in a slot, which experts_sum_kernel
-// adds in order (it also writes the zeros of experts without rows).
+// adds in order (it also writes the zeros of experts without rows; where no
+// expert can have two chunks, it is not needed).
 struct TokenJob {
   const uint16_t* X;   // M x ld
   int64_t J, ld;       // columns that count, row length
@@ -906,6 +920,8 @@ struct TokenJob {
 struct TokenArgs {
   TokenJob job[2];
   int first;           // workgroups of job 0
+  int single;          // every expert's rows are one chunk: a row of workgroups to each expert, also to those
+                       // without rows, whose zeros they write
   ExpertRows er;
   int R;
   float s;
@@ -943,7 +959,12 @@ __global__ __launch_bounds__(64 * WAVES) void experts_token_kernel(TokenArgs a) 
   const TokenJob& job = a.job[which];
   const int bid = (int)blockIdx.x - (which ? a.first : 0);
   Span sp;
-  if (!find_span(a.er, job.chunk, [&](int) { return bid / job.tiles; }, sp)) return;
+  if (a.single) {
+    sp = expert_span(a.er, job.chunk, bid / job.tiles);
+    sp.tiles = 1;
+  } else if (!find_span(a.er, job.chunk, [&](int) { return bid / job.tiles; }, sp)) {
+    return;
+  }
   const int R = a.R;
   const int64_t J = job.J, ld = job.ld;
   const int tid = threadIdx.x;
@@ -1117,7 +1138,7 @@ size_t experts_token_ws_bytes(int64_t M, int64_t J, int R) {
   return (size_t)(2 * M / token_chunk(M, J, R)) * J * R * sizeof(float);
 }
 
-bool experts_token_fits(int64_t M, int64_t E, int64_t J) { return most_tiles(M, E, 256) * cdiv(J, 128) < ((int64_t)1 << 30); }
+bool experts_token_fits(int64_t M, int64_t E, int64_t J) { return (M / 256 + E) * cdiv(J, 128) < ((int64_t)1 << 30); }
 
 void launch_experts_token(const uint16_t* x, const uint16_t* vplanes, uint16_t* grad_A, float* part_a,
                           const uint16_t* g, int64_t g_ld, const uint16_t* uplanes, uint16_t* grad_B, float* part_b,
@@ -1130,14 +1151,17 @@ void launch_experts_token(const uint16_t* x, const uint16_t* vplanes, uint16_t* 
   a.er = ExpertRows{offsets, (int)E, (int)M};
   a.R = R;
   a.s = s;
-  a.first = (int)(most_tiles(M, E, a.job[0].chunk) * a.job[0].tiles);
-  const dim3 grid((unsigned)(a.first + most_tiles(M, E, a.job[1].chunk) * a.job[1].tiles));
+  a.single = M <= a.job[0].chunk && M <= a.job[1].chunk;
+  auto wgs = [&](const TokenJob& j) { return (a.single ? E : most_tiles(M, E, j.chunk)) * j.tiles; };
+  a.first = (int)wgs(a.job[0]);
+  const dim3 grid((unsigned)(a.first + wgs(a.job[1])));
   switch (rank_blocks(R)) {
     case 1: hipLaunchKernelGGL((experts_token_kernel<1, 3, 4>), grid, dim3(256), 0, stream, a); break;
     case 2: hipLaunchKernelGGL((experts_token_kernel<2, 3, 4>), grid, dim3(256), 0, stream, a); break;
     case 4: hipLaunchKernelGGL((experts_token_kernel<4, 3, 8>), grid, dim3(512), 0, stream, a); break;
     default: hipLaunchKernelGGL((experts_token_kernel<8, 3, 4>), grid, dim3(256), 0, stream, a); break;
   }
+  if (a.single) return;
   const int64_t most = (n > m ? n : m) * R;
   hipLaunchKernelGGL(experts_sum_kernel, dim3((unsigned)cdiv(most, kSumCells), (unsigned)E, 2), dim3(256), 0, stream,
                      a);
