@@ -210,9 +210,9 @@ struct AdamWConst {
 __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t tensors, AdamWConst c,
                                                          const float* __restrict__ clip) {
   const PlanView pv = plan_view(plan, tensors);
+  // Read first and tested last, so that its latency is not added to the others'.
+  // Not finite: gradients without a finite norm, no step.
   const float factor = clip ? clip[1] : 1.0f;
-  if (!(__builtin_fabsf(factor) < __builtin_inff())) return;  // gradients without a finite norm: no step
-  if ((int64_t)blockIdx.x >= pv.header[0]) return;
   const AdamWTensor T = pv.tensors[pv.owner[blockIdx.x]];
   const int64_t e = ((int64_t)blockIdx.x - T.chunk) * kChunk + 8 * (int)threadIdx.x;
   const int64_t left = T.count - e;  // lanes past the end stay for the blocks' maxima
@@ -231,6 +231,7 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
       v[j] = __builtin_fmaf(c.f2, v[j], c.g2 * x * x);
       p[j] = p[j] * c.decay - c.step_size * (m[j] / (__builtin_sqrtf(v[j] * c.inv_bc2) + c.eps));
     }
+    if (!(__builtin_fabsf(factor) < __builtin_inff())) return;
     store_f32x8(static_cast<float*>(T.m) + e, left, m);
     store_f32x8(static_cast<float*>(T.v) + e, left, v);
   } else {
@@ -284,7 +285,7 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
       const float denom = root * dv * c.inv_root_bc2 + c.eps;
       p[j] = p[j] * c.decay - c.step_size * ((m[j] < 0.0 ? -mf : mf) * __builtin_amdgcn_rcpf(denom));
     }
-    if (left <= 0) return;
+    if (left <= 0 || !(__builtin_fabsf(factor) < __builtin_inff())) return;
     store_codes8(static_cast<uint8_t*>(T.m) + e, left, mo);
     store_codes8(static_cast<uint8_t*>(T.v) + e, left, vo);
     if ((threadIdx.x & 15) == 0) {

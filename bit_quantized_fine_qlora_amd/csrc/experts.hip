@@ -294,13 +294,13 @@ __global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p,
   if (tid >= 64 * lg2::kMfmaWaves)
     gemm_producer<kBwd>(p, tab, lds, tid - 64 * lg2::kMfmaWaves, f0, t0, k0, ks, lora, 0, &lds_word, skew);
   else if (left > 192)
-    gemm_consumer<kBwd, kPieces, false>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, lg2::BT, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else if (left > 128)
-    gemm_consumer<kBwd, kPieces, false, 192>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 192, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else if (left > 64)
-    gemm_consumer<kBwd, kPieces, false, 128>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 128, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else
-    gemm_consumer<kBwd, kPieces, false, 64>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 64, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
 }
 
 // Finishes tiles that ran as K pieces: out = bf16(piece 0 + piece 1 + ...), in

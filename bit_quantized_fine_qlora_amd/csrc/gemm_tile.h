@@ -337,8 +337,9 @@ struct WaveTile {
 };
 
 // MFMA waves (512 threads): each owns a WF-feature x WT-token output tile.
-// kRows: tokens that the tile covers at most, 256, 192, 128 or 64.
-template <bool kBwd, bool kPieces, bool kSkip, int kRows = lg2::BT>
+// kRows: tokens that the tile covers at most, 256, 192, 128 or 64.  kPlain: the
+// tile is never split in two halves and nothing is added to it.
+template <bool kBwd, bool kPieces, bool kSkip, int kRows = lg2::BT, bool kPlain = false>
 __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds& lds, int tid, int64_t f0,
                                               int64_t t0, int k0, int nk, bool lora, int split, uint32_t* lds_word) {
   constexpr int WF = WaveTile<kBwd, kRows>::F;
@@ -501,67 +502,69 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
                                                (int)(poff + (i * NJ + j) * 1024), 0, 0);
     return;
   }
-  if (split) {
-    uint32_t* sync = p.split_sync + 2 * sidx;
-    if (tid == 0) *lds_word = __hip_atomic_fetch_add(sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    if (*lds_word == 0u) {
-      const brsrc_t r_out = make_rsrc(part_base, lg2::BF * lg2::BT * 4);
-#pragma unroll
-      for (int i = 0; i < NI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), r_out,
-                                                 (int)(poff + (i * NJ + j) * 1024), 0, kAuxDevice);
-      __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are done
+  if constexpr (!kPlain) {
+    if (split) {
+      uint32_t* sync = p.split_sync + 2 * sidx;
+      if (tid == 0) *lds_word = __hip_atomic_fetch_add(sync, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
-      if (tid == 0) __hip_atomic_store(sync + 1, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      return;
-    }
-    bool ready = false;
-    for (uint32_t it = 0; it < kSplitSpinLimit; ++it) {
-      if (__hip_atomic_load(sync + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0u) {
-        ready = true;
-        break;
+      if (*lds_word == 0u) {
+        const brsrc_t r_out = make_rsrc(part_base, lg2::BF * lg2::BT * 4);
+  #pragma unroll
+        for (int i = 0; i < NI; ++i)
+  #pragma unroll
+          for (int j = 0; j < NJ; ++j)
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), r_out,
+                                                   (int)(poff + (i * NJ + j) * 1024), 0, kAuxDevice);
+        __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's stores are done
+        __syncthreads();
+        if (tid == 0) __hip_atomic_store(sync + 1, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        return;
       }
-      __builtin_amdgcn_s_sleep(2);
+      bool ready = false;
+      for (uint32_t it = 0; it < kSplitSpinLimit; ++it) {
+        if (__hip_atomic_load(sync + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) != 0u) {
+          ready = true;
+          break;
+        }
+        __builtin_amdgcn_s_sleep(2);
+      }
+      // A wait that runs out leaves the tile without the other half's sum:
+      // the give-up word after the hand-off words records it for the host
+      // (qlora_linear_check), instead of the tile being wrong silently.
+      if (!ready && tid == 0)
+        __hip_atomic_store(p.split_sync + 2 * p.nsplit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      part_bytes = lg2::BF * lg2::BT * 4;
     }
-    // A wait that runs out leaves the tile without the other half's sum:
-    // the give-up word after the hand-off words records it for the host
-    // (qlora_linear_check), instead of the tile being wrong silently.
-    if (!ready && tid == 0)
-      __hip_atomic_store(p.split_sync + 2 * p.nsplit, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    part_bytes = lg2::BF * lg2::BT * 4;
-  }
-  {
-    const brsrc_t r_part = make_rsrc(part_base, part_bytes);
-    // one row of fragments in flight at a time; the empty asm pins each sum
-    // in its accumulator registers (otherwise the adds sink to the stores
-    // below and the loaded values are spilled)
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        acc[i][j] += __builtin_bit_cast(
-            f32x4, __builtin_amdgcn_raw_buffer_load_b128(r_part, (int)(poff + (i * NJ + j) * 1024), 0, kAuxDevice));
-        asm volatile("" : "+v"(acc[i][j]));
+    {
+      const brsrc_t r_part = make_rsrc(part_base, part_bytes);
+      // one row of fragments in flight at a time; the empty asm pins each sum
+      // in its accumulator registers (otherwise the adds sink to the stores
+      // below and the loaded values are spilled)
+  #pragma unroll
+      for (int i = 0; i < NI; ++i) {
+  #pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          acc[i][j] += __builtin_bit_cast(
+              f32x4, __builtin_amdgcn_raw_buffer_load_b128(r_part, (int)(poff + (i * NJ + j) * 1024), 0, kAuxDevice));
+          asm volatile("" : "+v"(acc[i][j]));
+        }
       }
     }
-  }
-  if (p.add) {
-    // an fp32 term of the output computed elsewhere, added once per tile
-    // before the single rounding (M N 4 < 2^32 bytes; rows past M read 0)
-    const uint32_t add_bytes = (uint32_t)(p.M * p.N * 4);
-    const brsrc_t r_add = make_rsrc(p.add, add_bytes);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int64_t t = t0 + wt + 16 * j + lr;
-        const int64_t f = f0 + wf + 16 * i + 4 * lq;
-        const bool ok = t < p.M && f < p.N;
-        acc[i][j] += __builtin_bit_cast(f32x4, bload128(r_add, ok ? (uint32_t)((t * p.N + f) * 4) : add_bytes));
-        asm volatile("" : "+v"(acc[i][j]));
+    if (p.add) {
+      // an fp32 term of the output computed elsewhere, added once per tile
+      // before the single rounding (M N 4 < 2^32 bytes; rows past M read 0)
+      const uint32_t add_bytes = (uint32_t)(p.M * p.N * 4);
+      const brsrc_t r_add = make_rsrc(p.add, add_bytes);
+  #pragma unroll
+      for (int i = 0; i < NI; ++i) {
+  #pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const int64_t t = t0 + wt + 16 * j + lr;
+          const int64_t f = f0 + wf + 16 * i + 4 * lq;
+          const bool ok = t < p.M && f < p.N;
+          acc[i][j] += __builtin_bit_cast(f32x4, bload128(r_add, ok ? (uint32_t)((t * p.N + f) * 4) : add_bytes));
+          asm volatile("" : "+v"(acc[i][j]));
+        }
       }
     }
   }
