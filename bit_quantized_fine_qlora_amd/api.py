@@ -7,6 +7,7 @@ libqlora.so.  Torch supplies device memory (outputs and workspaces).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 
@@ -644,8 +645,24 @@ def preference_bwd(logits: torch.Tensor, labels: torch.Tensor, saved: Preference
     return out
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(device):
+    """The device to launch on made current, where it is not."""
+    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name}: must be on {device}, got one on {t.device}")
+
+
 def _experts(x, offsets, q, A, B):
     """(M, E, n, m, r) of the experts' layer, its operands checked."""
+    if isinstance(x, Checkpoint8):
+        raise TypeError("x: the experts' layer takes a bf16 tensor, not a Checkpoint8")
     M, n = x.shape
     if A.dim() != 3 or B.dim() != 3:
         raise ValueError("A, B: expected [experts, r, n] and [experts, m, r], got "
@@ -658,6 +675,11 @@ def _experts(x, offsets, q, A, B):
     _need(offsets, torch.int32, (E + 1,), "offsets")
     _need(A, torch.bfloat16, (E, r, n), "A")
     _need(B, torch.bfloat16, (E, m, r), "B")
+    cells = q.m * q.n
+    _need(q.codes, torch.uint8, (cells // 2,), "q.codes")
+    _need(q.absmax8, torch.uint8, (cells // 64,), "q.absmax8")
+    _need(q.c2, torch.float32, (-(-cells // 16384),), "q.c2")
+    _same_device(x.device, offsets=offsets, A=A, B=B, q=q.codes)
     return M, E, n, m, r
 
 
@@ -684,10 +706,12 @@ def experts_fwd(x: torch.Tensor, offsets: torch.Tensor, q: QuantizedWeight, A: t
         _need(u, torch.float32, (M, r), "u")
     elif want_u:
         u = torch.empty((M, r), dtype=torch.float32, device=x.device)
-    ws = _room(experts_workspace_bytes(QLORA_OP_FWD, M, E, n, m, r), x.device, workspace)
-    st = _lib.load().qlora_experts_fwd(M, E, n, m, r, float(s), _ptr(x), _ptr(offsets), _ptr(q.codes),
-                                       _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(h), _ptr(u), _ptr(ws),
-                                       ws.numel(), _stream(x.device))
+    _same_device(x.device, h=h, u=u)
+    with _on(x.device):
+        ws = _room(experts_workspace_bytes(QLORA_OP_FWD, M, E, n, m, r), x.device, workspace)
+        st = _lib.load().qlora_experts_fwd(M, E, n, m, r, float(s), _ptr(x), _ptr(offsets), _ptr(q.codes),
+                                           _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(h), _ptr(u), _ptr(ws),
+                                           ws.numel(), _stream(x.device))
     _lib.check(st, "qlora_experts_fwd")
     return h, u
 
@@ -713,10 +737,12 @@ def experts_bwd(x: torch.Tensor, g: torch.Tensor, offsets: torch.Tensor, q: Quan
             _need(gx, torch.bfloat16, (M, n), "out[0]")
         _need(gA, torch.bfloat16, (E, r, n), "out[1]")
         _need(gB, torch.bfloat16, (E, m, r), "out[2]")
-    ws = _room(experts_workspace_bytes(QLORA_OP_BWD, M, E, n, m, r), x.device, workspace)
-    st = _lib.load().qlora_experts_bwd(M, E, n, m, r, float(s), _ptr(x), _ptr(g), _ptr(offsets), _ptr(q.codes),
-                                       _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(u), _ptr(gx), _ptr(gA),
-                                       _ptr(gB), _ptr(ws), ws.numel(), _stream(x.device))
+    _same_device(x.device, g=g, u=u, **{"out[0]": gx, "out[1]": gA, "out[2]": gB})
+    with _on(x.device):
+        ws = _room(experts_workspace_bytes(QLORA_OP_BWD, M, E, n, m, r), x.device, workspace)
+        st = _lib.load().qlora_experts_bwd(M, E, n, m, r, float(s), _ptr(x), _ptr(g), _ptr(offsets), _ptr(q.codes),
+                                           _ptr(q.absmax8), _ptr(q.c2), _ptr(A), _ptr(B), _ptr(u), _ptr(gx),
+                                           _ptr(gA), _ptr(gB), _ptr(ws), ws.numel(), _stream(x.device))
     _lib.check(st, "qlora_experts_bwd")
     return gx, gA, gB
 
@@ -759,8 +785,11 @@ def moment8_values(moment: Moment8, out: torch.Tensor | None = None) -> torch.Te
         out = torch.empty(n, dtype=torch.float32, device=moment.codes.device)
     else:
         _need(out, torch.float32, (n,), "out")
-    st = _lib.load().qlora_moment8_values(0 if moment.signed else 1, n, _ptr(moment.codes), _ptr(moment.steps),
-                                          _ptr(out), _stream(moment.codes.device))
+    _need(moment.steps, torch.float32, tuple(moment.steps.shape), "moment.steps")
+    _same_device(moment.codes.device, out=out, **{"moment.steps": moment.steps})
+    with _on(moment.codes.device):
+        st = _lib.load().qlora_moment8_values(0 if moment.signed else 1, n, _ptr(moment.codes), _ptr(moment.steps),
+                                              _ptr(out), _stream(moment.codes.device))
     _lib.check(st, "qlora_moment8_values")
     return out
 
@@ -826,8 +855,9 @@ class AdamWStep:
         need = int(lib.qlora_adamw_plan_bytes(arr, len(self._keep)))
         self._plan = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
         self._handle = _lib.AdamWHandle()
-        st = lib.qlora_adamw_plan(arr, len(self._keep), _ptr(self._plan), self._plan.numel(),
-                                  ctypes.byref(self._handle), _stream(self.device))
+        with _on(self.device):
+            st = lib.qlora_adamw_plan(arr, len(self._keep), _ptr(self._plan), self._plan.numel(),
+                                      ctypes.byref(self._handle), _stream(self.device))
         _lib.check(st, "qlora_adamw_plan")
 
     def clip(self, max_norm: float, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -837,7 +867,10 @@ class AdamWStep:
             out = torch.empty(2, dtype=torch.float32, device=self.device)
         else:
             _need(out, torch.float32, (2,), "out")
-        st = _lib.load().qlora_grad_clip(ctypes.byref(self._handle), float(max_norm), _ptr(out), _stream(self.device))
+            _same_device(self.device, out=out)
+        with _on(self.device):
+            st = _lib.load().qlora_grad_clip(ctypes.byref(self._handle), float(max_norm), _ptr(out),
+                                             _stream(self.device))
         _lib.check(st, "qlora_grad_clip")
         return out
 
@@ -847,9 +880,11 @@ class AdamWStep:
         where that is NaN the step is not taken."""
         if clip is not None:
             _need(clip, torch.float32, (2,), "clip")
-        st = _lib.load().qlora_adamw_step(ctypes.byref(self._handle), float(lr), float(beta1), float(beta2),
-                                          float(eps), float(weight_decay), int(step), _ptr(clip),
-                                          _stream(self.device))
+            _same_device(self.device, clip=clip)
+        with _on(self.device):
+            st = _lib.load().qlora_adamw_step(ctypes.byref(self._handle), float(lr), float(beta1), float(beta2),
+                                              float(eps), float(weight_decay), int(step), _ptr(clip),
+                                              _stream(self.device))
         _lib.check(st, "qlora_adamw_step")
 
 

@@ -1206,22 +1206,22 @@ qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
   if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
   float* const u = u_out ? u_out : at<float>(workspace, w.u);
+  float* const part = at<float>(workspace, w.part);
+  const bool streamed = experts_stream_takes(M, E, m, n);  // then u's splits are summed where they are used
   {
     Timed tm("experts_down", hs);
-    float* const part = at<float>(workspace, w.part);
     launch_experts_down(x, offsets, M, E, n, A, false, n, r, part, w.splits, hs);
-    if (experts_stream_takes(M, E, m, n)) {
-      launch_experts_stream(offsets, E, x, codes, absmax8, c2, B, part, w.splits, u_out, h, M, n, m, r, s,
-                            at<uint8_t>(workspace, w.pieces), table(), hs);
-      return hip_status();
-    }
     const FactorJob job{part, w.splits, u, nullptr};
-    launch_experts_factor(&job, 1, offsets, M, E, r, hs);
+    if (!streamed) launch_experts_factor(&job, 1, offsets, M, E, r, hs);
   }
   {
     Timed tm("experts_fwd_gemm", hs);
-    launch_experts_gemm(false, offsets, E, x, codes, absmax8, c2, B, u, h, M, n, n, m, r, s,
-                        at<uint8_t>(workspace, w.pieces), table(), hs);
+    if (streamed)
+      launch_experts_stream(offsets, E, x, codes, absmax8, c2, B, part, w.splits, u_out, h, M, n, m, r, s,
+                            at<uint8_t>(workspace, w.pieces), table(), hs);
+    else
+      launch_experts_gemm(false, offsets, E, x, codes, absmax8, c2, B, u, h, M, n, n, m, r, s,
+                          at<uint8_t>(workspace, w.pieces), table(), hs);
   }
   return hip_status();
 }
@@ -1266,15 +1266,15 @@ qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
     }
     launch_experts_factor(jobs, 2, offsets, M, E, r, hs);
   }
-  if (grad_x) {
-    Timed tm("experts_dgrad_gemm", hs);
-    launch_experts_gemm(true, offsets, E, gk, codes, absmax8, c2, A, v, grad_x, M, w.m_pad, n, m, r, s,
-                        at<uint8_t>(workspace, w.pieces), table(), hs);
-  }
   {
     Timed tm("experts_token", hs);
     launch_experts_token(x, vplanes, grad_A, at<float>(workspace, w.gA), gk, w.m_pad, uplanes, grad_B,
                          at<float>(workspace, w.gB), offsets, M, E, n, m, r, s, hs);
+  }
+  if (grad_x) {
+    Timed tm("experts_dgrad_gemm", hs);
+    launch_experts_gemm(true, offsets, E, gk, codes, absmax8, c2, A, v, grad_x, M, w.m_pad, n, m, r, s,
+                        at<uint8_t>(workspace, w.pieces), table(), hs);
   }
   return hip_status();
 }

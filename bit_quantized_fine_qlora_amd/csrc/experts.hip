@@ -366,9 +366,16 @@ static int pieces_slots(int64_t M, int64_t E, int64_t N, int64_t K) {
   return gemm_tiles(M, E, N) <= device_cus() && cdiv(K, lg2::BK) >= 16 ? device_cus() : 0;
 }
 
-// tiles x pieces is at most the CUs where there are pieces
+// Work items in pieces, at most: as many as slots, and 16 (or one for 8 K
+// steps) to a tile.
+static int64_t pieces_items(int64_t M, int64_t E, int64_t N, int64_t K) {
+  const int64_t slots = pieces_slots(M, E, N, K), most = cdiv(K, lg2::BK) / 8;
+  const int64_t all = gemm_tiles(M, E, N) * (most < 16 ? most : 16);
+  return all < slots ? all : slots;
+}
+
 size_t experts_gemm_ws_bytes(int64_t M, int64_t E, int64_t N, int64_t K) {
-  return (size_t)pieces_slots(M, E, N, K) * lg2::BF * lg2::BT * sizeof(float);
+  return (size_t)pieces_items(M, E, N, K) * lg2::BF * lg2::BT * sizeof(float);
 }
 
 // bwd: act = g (M x K, K = m or m rounded up to 64 with zero columns), out =
@@ -397,7 +404,7 @@ void launch_experts_gemm(bool bwd, const int32_t* offsets, int64_t E, const uint
   if (!slots) return;
   p.piece_out = static_cast<float*>(ws);
   // at most half the slots in tiles
-  const dim3 pgrid((unsigned)slots);
+  const dim3 pgrid((unsigned)pieces_items(M, E, p.N, K));
   const dim3 rgrid((unsigned)((tiles < slots / 2 ? tiles : slots / 2) * (lg2::BF * lg2::BT / 4 / 256)));
   if (bwd) {
     hipLaunchKernelGGL((experts_gemm_kernel<true, true>), pgrid, block, 0, stream, p, er, tab, slots);
@@ -611,6 +618,7 @@ __global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, Ex
   constexpr int kAfter = (NS - 2) * XL + CL * ((ND < NS ? ND : NS) - 1);
   auto step = [&](int s, int u) {
     wait_vmcnt<kAfter>();
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the reads of the stage that is loaded next are done
     ring_barrier();
     issue_x(s + NS - 1, buf4[(u + NS - 1) % NS]);
     fence();
@@ -1050,6 +1058,7 @@ __global__ __launch_bounds__(64 * WAVES) void experts_token_kernel(TokenArgs a) 
         }
       }
     }
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage's reads are done before the barrier that frees it
   };
   ring_run<NS, LMIN>(nst, buf, issue, compute);
 

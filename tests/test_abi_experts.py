@@ -180,5 +180,7 @@ def test_binding_refuses_experts_of_other_shapes():
             Q.experts_fwd(*args)
     with pytest.raises(TypeError):
         Q.experts_fwd(x.float(), off, q, A, B, 1.0)
+    with pytest.raises(TypeError, match="Checkpoint8"):
+        Q.experts_bwd(Q.alloc_checkpoint(M, n, "cpu"), torch.zeros(M, m, **bf), off, q, A, B, 1.0)
     with pytest.raises(ValueError, match="device tensor"):
         Q.experts_fwd(x, off, q, A, B, 1.0)
