@@ -812,42 +812,58 @@ class AdamWStep:
             device = torch.device(device)
             if device.index is None:
                 device = torch.device(device.type, torch.cuda.current_device())
+        index = -1 if device is None else device.index
         arr = (_lib.AdamWTensor * len(self._keep))()
+        spans = []  # (first byte, end, tensor, written)
         for i, (p, p16, g, m, v) in enumerate(self._keep):
             n = p.numel()
             eight = isinstance(m, Moment8)
             if eight != isinstance(v, Moment8):
                 raise TypeError("exp_avg and exp_avg_sq: both Moment8 or neither")
-            named = [(p, "param", torch.float32), (g, "grad", g.dtype)]
+            named = [("grad", g, g.dtype, n), ("param", p, torch.float32, n)]
             if p16 is not None:
-                named.append((p16, "param_bf16", torch.bfloat16))
+                named.append(("param_bf16", p16, torch.bfloat16, n))
             if eight:
                 if not m.signed or v.signed:
                     raise ValueError("exp_avg must be a signed Moment8, exp_avg_sq one that is not")
-                m.check("exp_avg", n)
-                v.check("exp_avg_sq", n)
-                moments = [(m.codes, "exp_avg", None), (m.steps, "exp_avg", None), (v.codes, "exp_avg_sq", None),
-                           (v.steps, "exp_avg_sq", None)]
+                steps = -(-n // MOMENT_BLOCK)
+                named += [("exp_avg.codes", m.codes, torch.uint8, n), ("exp_avg.steps", m.steps, torch.float32, steps),
+                          ("exp_avg_sq.codes", v.codes, torch.uint8, n),
+                          ("exp_avg_sq.steps", v.steps, torch.float32, steps)]
             else:
-                moments = [(m, "exp_avg", torch.float32), (v, "exp_avg_sq", torch.float32)]
-                named += moments
+                named += [("exp_avg", m, torch.float32, n), ("exp_avg_sq", v, torch.float32, n)]
             gtype = _type_of(g, "grad")
-            for t, nm, dtype in named:
-                if t.dtype != dtype:
+            ptrs = []
+            for nm, t, dtype, count in named:
+                if t.dtype is not dtype:
                     raise TypeError(f"{nm}: expected {dtype}, got {t.dtype}")
-                if t.numel() != n or not t.is_contiguous():
-                    raise ValueError(f"{nm}: expected {n} contiguous elements")
-            for t, nm, _ in named + moments:
-                if t.is_cuda:
-                    if device is None:
-                        device = t.device
-                    if t.device != device:
-                        raise ValueError(f"{nm}: all tensors must be on {device}, got one on {t.device}")
-                elif not t.is_pinned():
-                    raise ValueError(f"{nm}: must be on the GPU or in pinned host memory")
-            arr[i] = _lib.AdamWTensor(n, _ptr(p), _ptr(p16), _ptr(g), _ptr(m.codes if eight else m),
-                                      _ptr(v.codes if eight else v), _ptr(m.steps) if eight else None,
-                                      _ptr(v.steps) if eight else None, gtype, int(eight))
+                if t.numel() != count or not t.is_contiguous():
+                    raise ValueError(f"{nm}: expected {count} contiguous elements")
+            for nm, t, dtype, count in named:
+                on = t.get_device()
+                if on < 0:
+                    if not t.is_pinned():
+                        raise ValueError(f"{nm}: must be on the GPU or in pinned host memory")
+                elif index < 0:
+                    index, device = on, t.device
+                elif on != index:
+                    raise ValueError(f"{nm}: all tensors must be on {device}, got one on {t.device}")
+                ptr = t.data_ptr()
+                spans.append((ptr, ptr + count * t.element_size(), i, nm != "grad"))
+                ptrs.append(ptr)
+            at = 2 if p16 is None else 3  # the moments'
+            rest = (ptrs[at], ptrs[at + 2], ptrs[at + 1], ptrs[at + 3]) if eight else (*ptrs[at:], None, None)
+            arr[i] = (n, ptrs[1], None if p16 is None else ptrs[2], ptrs[0], *rest, gtype, int(eight))
+        spans.sort()
+        read, wrote = (0, 0), (0, 0)  # the furthest end so far, and whose it is
+        for begin, end, i, writes in spans:
+            if begin < wrote[0] or (writes and begin < read[0]):
+                k = wrote[1] if begin < wrote[0] else read[1]
+                raise ValueError(f"tensors {k} and {i}: the step would write memory that they share")
+            if writes:
+                wrote = max(wrote, (end, i))
+            else:
+                read = max(read, (end, i))
         if device is None:
             device = torch.device("cuda", torch.cuda.current_device())
         self.device = device

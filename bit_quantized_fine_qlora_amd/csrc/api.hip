@@ -431,8 +431,11 @@ qlora_status check_experts(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r
   return st;
 }
 
+constexpr int64_t kMaxChunks = (int64_t)1 << 24;         // not reached: 256 threads each, fewer than 2^32 in a launch
+constexpr int64_t kMaxCount = (kMaxChunks - 1) * 2048;   // elements of as many
+
 qlora_status check_adamw_tensor(const qlora_adamw_tensor& t) {
-  if (t.count < 1 || t.count >= ((int64_t)1 << 40)) return QLORA_ERR_SHAPE;
+  if (t.count < 1 || t.count > kMaxCount) return QLORA_ERR_SHAPE;
   if ((t.grad_type != QLORA_BF16 && t.grad_type != QLORA_F32) ||
       (t.moments != QLORA_MOMENTS_F32 && t.moments != QLORA_MOMENTS_8BIT))
     return QLORA_ERR_VALUE;
@@ -454,14 +457,14 @@ int64_t adamw_total_chunks(const qlora_adamw_tensor* tensors, int64_t count) {
     const qlora_status st = check_adamw_tensor(tensors[i]);
     if (st != QLORA_OK) return st;
     chunks += adamw_chunks(tensors[i].count);
-    if (chunks >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
+    if (chunks >= kMaxChunks) return QLORA_ERR_SHAPE;
   }
   return chunks;
 }
 
 qlora_status check_adamw_handle(const qlora_adamw_handle* h) {
   if (!h || !h->plan) return QLORA_ERR_NULL;
-  if (h->tensors < 1 || h->chunks < 1 || h->chunks >= ((int64_t)1 << 31)) return QLORA_ERR_SHAPE;
+  if (h->tensors < 1 || h->chunks < 1 || h->chunks >= kMaxChunks) return QLORA_ERR_SHAPE;
   return aligned16(h->plan) ? QLORA_OK : QLORA_ERR_ALIGN;
 }
 
@@ -1343,7 +1346,7 @@ qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, doubl
 qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* codes, const float* steps, float* out,
                                   qlora_stream_t stream) {
   if (second != 0 && second != 1) return QLORA_ERR_VALUE;
-  if (count < 1 || count >= ((int64_t)1 << 40)) return QLORA_ERR_SHAPE;
+  if (count < 1 || count > kMaxCount) return QLORA_ERR_SHAPE;
   if (!codes || !steps || !out) return QLORA_ERR_NULL;
   if (!aligned16(codes) || !aligned4(steps) || !aligned16(out)) return QLORA_ERR_ALIGN;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);

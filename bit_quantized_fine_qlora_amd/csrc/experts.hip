@@ -70,7 +70,8 @@ struct ExpertScan {
   int first = 0;               // expert of lane 0
   int end = 0;                 // last row + 1 of the experts before
   int tiles = 0, slots = 0;    // of the experts before
-  int row0 = 0, rows = 0, t = 0, t_incl = 0, s_incl = 0;  // of this lane's expert, and with those of the lanes below
+  int row0 = 0, rows = 0, t = 0;  // of this lane's expert
+  int t_incl = 0, s_incl = 0;     // with those of the lanes below
 
   __device__ __forceinline__ static int held(int v, int M) { return v < 0 ? 0 : v > M ? M : v; }
   __device__ __forceinline__ void begin(const ExpertRows& r) {
@@ -357,7 +358,8 @@ __global__ __launch_bounds__(256) void experts_pieces_kernel(GemmArgs p, ExpertR
 
 static int64_t gemm_tiles(int64_t M, int64_t E, int64_t N) { return most_tiles(M, E, lg2::BT) * cdiv(N, lg2::BF); }
 
-bool experts_gemm_fits(int64_t M, int64_t E, int64_t N) { return gemm_tiles(M, E, N) < ((int64_t)1 << 24); }
+// Fewer than 2^32 threads in a launch.
+bool experts_gemm_fits(int64_t M, int64_t E, int64_t N) { return gemm_tiles(M, E, N) < ((int64_t)1 << 22); }
 
 // Workgroups for K pieces: none where there will hardly be as few tiles as
 // half the CUs (the bound counts a ragged tile to every expert), or where K is
@@ -481,19 +483,14 @@ template <int TB>
 __global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, ExpertRows er, Nf4Table tab) {
   constexpr int NW = 4;                  // waves
   constexpr int NF = 2;                  // blocks of 16 features of a wave
-  constexpr int NS = 2;                  // stages of x in LDS
-  constexpr int ND = 2;                  // pieces of codes in registers
   constexpr int BT = 16 * TB;
   constexpr int STAGE = BT * 512;        // 256 k of each row
   constexpr int XL = TB * 8 / NW;        // 1 KB loads of x per wave and stage
   constexpr int CL = 4 * NF;             // loads of a piece of codes
-  constexpr int U = NS > ND ? NS : ND;
-  static_assert(U % NS == 0 && U % ND == 0 && TB * 8 % NW == 0, "ring");
+  static_assert(TB * 8 % NW == 0, "loads of x");
   __shared__ __align__(16) uint8_t s0[STAGE];
   __shared__ __align__(16) uint8_t s1[STAGE];
-  __shared__ __align__(16) uint8_t s2[NS > 2 ? STAGE : 16];
-  __shared__ __align__(16) uint8_t s3[NS > 3 ? STAGE : 16];
-  uint8_t* const buf4[4] = {s0, s1, s2, s3};
+  uint8_t* const buf[2] = {s0, s1};
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -519,7 +516,6 @@ __global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, Ex
   const int pb = split * pieces / p.ksplits, pe = (split + 1) * pieces / p.ksplits;
   const int nst = pe - pb;
   const int t0 = tile * BT;
-  const int nt = (sp.rows - t0 + 15) / 16 < TB ? (sp.rows - t0 + 15) / 16 : TB;  // blocks with rows
 
   const int64_t cells = p.N * K;
   const int64_t block0 = sp.e * (cells / kBlock);
@@ -542,7 +538,8 @@ __global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, Ex
       const int row = 2 * blk + (lane >> 5);
       const int c = (lane & 31) ^ (row & 15);  // slot -> 16 (g % 2) + 8 (g / 2) + q
       const int64_t k = (int64_t)(pb + s) * 256 + 64 * ((c >> 4) | ((c >> 2) & 2)) + 8 * (c & 7);
-      dma16(rx, stg + blk * 1024, s < nst && k < K && t0 + row < sp.rows ? (uint32_t)(((t0 + row) * K + k) * 2) : xbytes);
+      const bool live = s < nst && k < K && t0 + row < sp.rows;
+      dma16(rx, stg + blk * 1024, live ? (uint32_t)(((t0 + row) * K + k) * 2) : xbytes);
     }
   };
   // codes: a lane takes one 64-weight block of feature row lr for each of the
@@ -602,38 +599,33 @@ __global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, Ex
         for (int b = 0; b < NF; ++b) acc[b][t] = mfma16x16x32(w[b], xf[q & 1][t], acc[b][t]);
     }
   };
-  // Per step: the wave's loads of stage s have landed when no more are in
-  // flight than were issued after them (loads complete in order; the empty
-  // asm keeps the order of issue); the barrier makes that so for all waves,
-  // and frees the stage before.  Steps past the end load nothing.
+  // Two stages of x and two pieces of codes: while one is multiplied the next
+  // is on its way.  A step begins when the wave's loads of its x have landed
+  // (loads complete in order and only the piece's codes were issued after them;
+  // the empty asm keeps the order of issue) and all waves have read the stage
+  // before, which is then loaded anew.  Steps past the end load nothing.
   auto fence = []() { asm volatile("" ::: "memory"); };
-  Piece P[ND];
-#pragma unroll
-  for (int j = -(NS > ND ? NS - 1 : ND - 1); j < 0; ++j) {
-    if (j >= -(NS - 1)) issue_x(j + NS - 1, buf4[j + NS - 1]);
-    fence();
-    if (j >= -(ND - 1)) load(j + ND - 1, P[j + ND - 1]);
-    fence();
-  }
-  constexpr int kAfter = (NS - 2) * XL + CL * ((ND < NS ? ND : NS) - 1);
+  Piece P[2];
+  issue_x(0, buf[0]);
+  fence();
+  load(0, P[0]);
+  fence();
   auto step = [&](int s, int u) {
-    wait_vmcnt<kAfter>();
+    wait_vmcnt<CL>();
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the reads of the stage that is loaded next are done
     ring_barrier();
-    issue_x(s + NS - 1, buf4[(u + NS - 1) % NS]);
+    issue_x(s + 1, buf[u ^ 1]);
     fence();
-    load(s + ND - 1, P[(u + ND - 1) % ND]);
+    load(s + 1, P[u ^ 1]);
     fence();
-    compute(buf4[u % NS], P[u % ND]);
+    compute(buf[u], P[u]);
   };
-  const int full = nst - nst % U;
-  for (int sb = 0; sb < full; sb += U) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) step(sb + u, u);
+  int st = 0;
+  for (; st + 1 < nst; st += 2) {
+    step(st, 0);
+    step(st + 1, 1);
   }
-#pragma unroll
-  for (int u = 0; u < U - 1; ++u)
-    if (full + u < nst) step(full + u, u);
+  if (st < nst) step(st, 0);
   wait_vmcnt<0>();
 
   // lane holds features f0 + 16 b + 4 g + e of row t0 + 16 t + lr.  The LoRA
@@ -762,7 +754,8 @@ void launch_experts_stream(const int32_t* offsets, int64_t E, const uint16_t* x,
                            float* u_out, uint16_t* h, int64_t M, int64_t n, int64_t m, int r, float s, void* ws,
                            const Nf4Table& tab, hipStream_t stream) {
   const StreamPlan plan = stream_plan(M, E, m, n);
-  StreamArgs p{x, codes, absmax8, c2, B, u, usplits, u_out, h, static_cast<float*>(ws), plan.ksplits, n, m, r, s, plan.groups};
+  const StreamArgs p{x,     codes, absmax8, c2, B, u, usplits, u_out, h, static_cast<float*>(ws), plan.ksplits,
+                     n,     m,     r,       s,  plan.groups};
   const ExpertRows er{offsets, (int)E, (int)M};
   const int64_t items = most_tiles(M, E, 16 * plan.tb) * plan.groups;
   const dim3 grid((unsigned)(cdiv(items, 8) * 8), (unsigned)plan.ksplits), block(64 * kStreamWaves);
@@ -839,18 +832,20 @@ __global__ __launch_bounds__(256) void experts_prepare_kernel(const uint16_t* __
     const int64_t t = i / ld, f = i % ld;
     gout[i] = f < m ? g[t * m + f] : (uint16_t)0;
   } else {
-    const int64_t i = ((int64_t)blockIdx.x - gblocks) * 256 + threadIdx.x;  // over E x R x ld
-    if (i >= bcount) return;
-    const int64_t f = i % ld, eq = i / ld;
-    const int64_t e = eq / R, q = eq % R;
-    bout[i] = f < m ? B[(e * m + f) * R + q] : (uint16_t)0;
+    int64_t i = ((int64_t)blockIdx.x - gblocks) * 256 + threadIdx.x;  // over E x R x ld
+    for (; i < bcount; i += ((int64_t)gridDim.x - gblocks) * 256) {
+      const int64_t f = i % ld, eq = i / ld;
+      const int64_t e = eq / R, q = eq % R;
+      bout[i] = f < m ? B[(e * m + f) * R + q] : (uint16_t)0;
+    }
   }
 }
 
 void launch_experts_prepare(const uint16_t* g, uint16_t* gout, const uint16_t* B, uint16_t* bout, int64_t M, int64_t E,
                             int64_t m, int R, int64_t ld, hipStream_t stream) {
   const int64_t gcount = gout ? M * ld : 0, bcount = bout ? E * R * ld : 0;
-  const int64_t gblocks = cdiv(gcount, 256), blocks = gblocks + cdiv(bcount, 256);
+  const int64_t gblocks = cdiv(gcount, 256), bblocks = cdiv(bcount, 256);  // gcount < 2^30
+  const int64_t blocks = gblocks + (bblocks < (1 << 20) ? bblocks : 1 << 20);
   if (blocks)
     hipLaunchKernelGGL(experts_prepare_kernel, dim3((unsigned)blocks), dim3(256), 0, stream, g, gcount, gout, B, bcount,
                        bout, m, R, ld, gblocks);
@@ -1147,7 +1142,10 @@ size_t experts_token_ws_bytes(int64_t M, int64_t J, int R) {
   return (size_t)(2 * M / token_chunk(M, J, R)) * J * R * sizeof(float);
 }
 
-bool experts_token_fits(int64_t M, int64_t E, int64_t J) { return (M / 256 + E) * cdiv(J, 128) < ((int64_t)1 << 30); }
+// Fewer than 2^32 threads in the launches of the products (two jobs, 512 threads at most) and of their sums.
+bool experts_token_fits(int64_t M, int64_t E, int64_t J) {
+  return (M / 256 + E) * cdiv(J, 128) < ((int64_t)1 << 22) && J < ((int64_t)1 << 27);
+}
 
 void launch_experts_token(const uint16_t* x, const uint16_t* vplanes, uint16_t* grad_A, float* part_a,
                           const uint16_t* g, int64_t g_ld, const uint16_t* uplanes, uint16_t* grad_B, float* part_b,

@@ -572,8 +572,9 @@ qlora_status qlora_preference_bwd(int32_t type, int64_t T, int64_t V, const void
  *            weight, expert e's rows e m .. (e + 1) m - 1.
  *   A        device, E x r x n bf16.      B  device, E x m x r bf16.
  *   x, h, u_out: as for qlora_linear_fwd, M rows in all; u_out may be NULL.
- * Requires 1 <= E <= 1024, M < 2^22, E m < 2^31, E m n <= 2^40, and for each
- * expert the limits of qlora_linear_fwd with all M rows.  No dropout.
+ * Requires 1 <= E <= 1024, M < 2^22, E m < 2^31, E m n <= 2^40,
+ * (M / 256 + E) ceil(max(n, m) / 128) < 2^22, and for each expert the limits
+ * of qlora_linear_fwd with all M rows.  No dropout.
  */
 #define QLORA_MAX_EXPERTS 1024
 qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
@@ -609,7 +610,8 @@ qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
 /*
  * One tensor of qlora_adamw_step (host struct; device-addressable pointers, as
  * for qlora_adam_tensor; grad in device memory or pinned host memory).
- *   count       elements (>= 1, < 2^40).
+ *   count       elements (>= 1; of chunks of 2048, begun anew for each tensor,
+ *               a plan holds fewer than 2^24).
  *   param       fp32 master weights, updated in place.
  *   param_bf16  bf16 copy written after the update, or NULL.
  *   grad        gradient of grad_type, QLORA_BF16 or QLORA_F32.
@@ -682,7 +684,8 @@ qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, doubl
 
 /*
  * The fp32 values that an 8-bit moment's `count` codes stand for; second: 0
- * for an exp_avg, 1 for an exp_avg_sq.  steps: 4-byte aligned.
+ * for an exp_avg, 1 for an exp_avg_sq.  steps: 4-byte aligned.  At most
+ * 2^35 - 2^11 codes.
  */
 qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* codes, const float* steps, float* out,
                                   qlora_stream_t stream);

@@ -356,6 +356,14 @@ def test_given_tensors_are_checked(Q):
         Q.AdamWStep([(f[1:129], None, f[:128].clone(), f[:128].clone(), f[:128].clone())])
     with pytest.raises(Q.QloraError):
         Q.AdamWStep([(f[:0], None, f[:0], f[:0], f[:0])])
+    g, h = f.clone(), torch.zeros(256, device="cuda")
+    new = lambda: [Q.alloc_moment8(256, True), Q.alloc_moment8(256, False)]
+    Q.AdamWStep([(f, None, g, *new()), (h, None, g, *new())])  # a gradient that two tensors read
+    for other in ((f, None, g.clone(), *new()), (h, None, g.clone(), m8, new()[1]), (h, None, f, *new()),
+                  (h, g[128:].view(torch.bfloat16), h.clone(), *new()), (h, None, h, *new())):
+        for pair in ([(f, None, g, m8, v8), other], [other, (f, None, g, m8, v8)]):
+            with pytest.raises(ValueError, match="share"):
+                Q.AdamWStep(pair)
     step_of = Q.AdamWStep([(f, None, f.clone(), m8, v8)])
     with pytest.raises(ValueError):
         step_of.run(1e-3, clip=torch.ones(2))
