@@ -218,11 +218,30 @@ static inline int64_t most_tiles(int64_t M, int64_t E, int64_t bt) { return M / 
 // ---------------------------------------------------------------------------
 // h and grad_x: the dense GEMM's tile on an expert's operands
 // ---------------------------------------------------------------------------
+// 2 rows N K operations against N K / 2 bytes of weights an expert: bound by
+// the matrix units from some 100 rows an expert on.  Measured, r = 16, x 8 of
+// 14336 x 4096 and 8192 rows (962 GFLOP): h 890-1030 us by card, grad_x 940-1050
+// us, 0.92-1.08 PFLOP/s; one dense layer of these sizes takes 770-850 and
+// 730-815 us on the same cards, the difference being the experts' ragged tiles.
+// 64 of 1024 x 2048 and 6000 ragged rows (25 GFLOP, 104 MB): 47 us, of which 14
+// go without any step of K (launch, finding the tile, first loads, epilogue)
+// and 31 are a chain of LDS reads, dequantization and MFMA in tiles of mostly
+// one expert's rows.
+//
+// Ragged tiles.  An expert's last tile has 1 .. 256 rows; its consumers take
+// the least of 64, 128, 192 and 256 rows that holds them, all waves sharing
+// whatever height it is (64 x 1024 x 2048: 56 us with heights of 128 and 256
+// only, 49 with these; 16 x 4096 x 4096, 192 rows an expert: 116 and 104).  As
+// a launch of their own the ragged tiles took as long (885 + 133 us against
+// 1030), and a tile of 128 x 128 twice to a compute unit more (64 x 1024 x
+// 2048: 62 us against 53 at that time; 8 x 14336 x 4096: 1267 against 1030).
+//
 // Few tiles run as K pieces, as in the dense layer: a piece to each of `slots`
 // workgroups (0: no pieces), with at least 8 K steps.  How many tiles there are
 // is only known here, so where there may be enough of them to go without, both
 // kernels are launched, and one of them ends at once (a kernel that could do
-// either would not have the registers).
+// either would not have the registers).  8 x 4096 x 14336, 192 rows an expert:
+// 333 us without pieces, 228 with them (207 with the heights above).
 __device__ __forceinline__ int pieces_of(int tiles, int slots, int nk) {
   int p = slots / (tiles > 0 ? tiles : 1);
   p = p < 16 ? p : 16;
@@ -460,6 +479,24 @@ __device__ __forceinline__ void lora_rows(const float* part, int splits, int64_t
 // ---------------------------------------------------------------------------
 // h where experts have few rows: weights straight into MFMA operands
 // ---------------------------------------------------------------------------
+// Every weight is read for a few rows, so the codes' bytes bound it.  A wave
+// takes 32 features, dequantizes a code's 8 weights right where the MFMA wants
+// them (a lane holds one 64-weight block of one feature, so one scale and one
+// table serve it for 8 MFMA steps) and never writes weights to LDS; only x goes
+// through it, shared by the workgroup's 128 features.  8 x 14336 x 4096 (235 MB
+// of codes, 16 rows): 64-65 us, 3.6 TB/s; the codes' loads alone take 54 us
+// (4.4 TB/s), with x and the barriers 59.  Loads arranged to 64 contiguous
+// bytes a row and swapped between lanes took 69 us, non-temporal loads 67.
+//
+// Whole calls, us, tiles of 16 rows / tiles of 32 / the GEMM, by rows an expert
+// (r = 16):
+//                            16               32               48
+//    8 x 14336 x 4096    67  74 109      102  77 107     152 118 107
+//    8 x 4096 x 14336    64  69 119      108  80 123     154 136 127
+//   16 x 4096 x 4096     38  42  60       63  45  60      87  72  60
+//   64 x 1024 x 2048     25  28  38       38  30  38      52  44  39
+// so tiles of 16 rows up to 16 rows an expert on average, of 32 up to 32, then
+// the GEMM.  Tiles of 64 and 128 rows were no better than it anywhere above.
 struct StreamArgs {
   const uint16_t* x;        // M x K
   const uint8_t* codes;
@@ -719,6 +756,9 @@ __global__ __launch_bounds__(256) void experts_stream_sum_kernel(StreamArgs p, E
   }
 }
 
+// Features go to workgroups of 4 waves, 32 a wave; K is split where the
+// workgroups would not fill the compute units four times, each split at least
+// two pieces of 256.
 struct StreamPlan {
   int tb;       // 16-row blocks of a tile, 0: the GEMM takes the call
   int groups;   // of 128 features
@@ -770,6 +810,11 @@ void launch_experts_stream(const int32_t* offsets, int64_t E, const uint16_t* x,
 // ---------------------------------------------------------------------------
 // u = x A_e^T and v = g B_e
 // ---------------------------------------------------------------------------
+// One read of x or g, which bounds it; the dense layer's tile of 128 rows on
+// an expert's rows.  K is split until the workgroups fill the chip once, and
+// experts_factor_kernel adds the splits in order.  8192 rows, r = 16: u of 4096
+// columns 16 us (67 MB, 4.2 TB/s), v of 14336 columns 56 us (235 MB, 4.2 TB/s);
+// 4096 rows of 8192 columns, r = 64: 23 us (2.9 TB/s: 5 stages a workgroup).
 
 // Y: A, E x [R][K], or (kYT) B, E x [yrows][R].
 template <int RB, bool kYT>
@@ -853,7 +898,8 @@ void launch_experts_prepare(const uint16_t* g, uint16_t* gout, const uint16_t* B
 
 // Sums the splits of u or v in order: fp32 out (may be null) and, for the
 // products over rows, bf16 hi and lo planes [M][16 RB] with zero ranks from R
-// on (planes may be null).  Rows outside every expert are left alone.
+// on (planes may be null).  Rows outside every expert are left alone.  8192
+// rows of 16 ranks, 7 splits: 4-5 us, its launch and one trip to memory.
 __global__ __launch_bounds__(256) void experts_factor_kernel(FactorJob a, FactorJob b, ExpertRows er, int R, int RP) {
   const FactorJob j = blockIdx.y ? b : a;
   const int i = (int)(blockIdx.x * 256 + threadIdx.x);  // rank pairs of all rows (fewer than 2^29)
@@ -908,7 +954,10 @@ void launch_experts_factor(const FactorJob* jobs, int count, const int32_t* offs
 // operands.  An expert whose rows are one chunk gets its gradient from here;
 // of more chunks each leaves fp32 sums in a slot, which experts_sum_kernel
 // adds in order (it also writes the zeros of experts without rows; where no
-// expert can have two chunks, it is not needed).
+// expert can have two chunks, it is not needed).  Bound by the read of x and
+// g.  Both products in one launch, 8192 rows of 4096 and 14336 columns, r = 16:
+// 61 us and 5 us for the sums (302 MB, 4.6 TB/s); 4096 rows of 28672 and 8192
+// columns, r = 64: 70 us and 8 us (3.9 TB/s).
 struct TokenJob {
   const uint16_t* X;   // M x ld
   int64_t J, ld;       // columns that count, row length
