@@ -648,8 +648,7 @@ __global__ __launch_bounds__(256, 4) void experts_stream_kernel(StreamArgs p, Ex
   load(0, P[0]);
   fence();
   auto step = [&](int s, int u) {
-    wait_vmcnt<CL>();
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the reads of the stage that is loaded next are done
+    wait_vmcnt_lds<CL>();
     ring_barrier();
     issue_x(s + 1, buf[u ^ 1]);
     fence();
@@ -1102,7 +1101,6 @@ __global__ __launch_bounds__(64 * WAVES) void experts_token_kernel(TokenArgs a) 
         }
       }
     }
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): this stage's reads are done before the barrier that frees it
   };
   ring_run<NS, LMIN>(nst, buf, issue, compute);
 

@@ -27,6 +27,15 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));
 }
 
+// The same with the wave's LDS reads done too (lgkmcnt(0)): in front of a
+// barrier behind which another wave may load into what they read.  The compiler
+// waits for a read where its value is used, which may be behind the barrier.
+template <int N>
+__device__ __forceinline__ void wait_vmcnt_lds() {
+  static_assert(N >= 0 && N < 64, "vmcnt holds 6 bits");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+}
+
 // One direct-to-LDS load of 16 bytes per lane: lane l writes bytes
 // 16 l .. 16 l + 15 of the 1 KB block at `blk`.
 __device__ __forceinline__ void dma16(brsrc_t r, uint8_t* blk, uint32_t voff) {
@@ -49,8 +58,8 @@ __device__ __forceinline__ void ring_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The ring: stage s lives in buffer s % NS; step s waits for stage s, issues
-// stage s + NS - 1 into the buffer of stage s - 1 (free after the barrier)
+// The ring: stage s lives in buffer s % NS; step s waits for stage s (and for
+// its own reads of stage s - 1), issues stage s + NS - 1 into the buffer of stage s - 1 (free after the barrier)
 // and computes stage s.  Loads are issued unconditionally: stages past the
 // end read only out-of-range offsets (zeros, no memory traffic) into buffers
 // nobody reads again.  So before the wait of step s exactly the stages
@@ -67,7 +76,7 @@ __device__ __forceinline__ void ring_run(int nst, uint8_t* const (&buf)[NS], Iss
 #pragma unroll
   for (int u = 0; u < NS - 1; ++u) issue(u, buf[u]);
   auto step = [&](int s, int u) {
-    wait_vmcnt<LMIN * (NS - 2)>();
+    wait_vmcnt_lds<LMIN * (NS - 2)>();
     ring_barrier();
     issue(s + NS - 1, buf[(u + NS - 1) % NS]);
     compute(buf[u]);
