@@ -810,10 +810,11 @@ void launch_experts_stream(const int32_t* offsets, int64_t E, const uint16_t* x,
 // u = x A_e^T and v = g B_e
 // ---------------------------------------------------------------------------
 // One read of x or g, which bounds it; the dense layer's tile of 128 rows on
-// an expert's rows.  K is split until the workgroups fill the chip once, and
-// experts_factor_kernel adds the splits in order.  8192 rows, r = 16: u of 4096
-// columns 16 us (67 MB, 4.2 TB/s), v of 14336 columns 56 us (235 MB, 4.2 TB/s);
-// 4096 rows of 8192 columns, r = 64: 23 us (2.9 TB/s: 5 stages a workgroup).
+// an expert's rows.  K is split until there is a workgroup to each compute
+// unit, and experts_factor_kernel adds the splits in order.  8192 rows, r = 16:
+// u of 4096 columns 16 us (67 MB, 4.2 TB/s), v of 14336 columns 46 us (235 MB,
+// 5.1 TB/s; with splits for two workgroups to a unit 56, for half of them 58);
+// 4096 rows of 8192 columns, r = 64: 22 us (3.0 TB/s).
 
 // Y: A, E x [R][K], or (kYT) B, E x [yrows][R].
 template <int RB, bool kYT>
@@ -830,8 +831,7 @@ __global__ __launch_bounds__(256) void experts_down_kernel(const uint16_t* __res
 static inline int rank_blocks(int R) { return R <= 16 ? 1 : R <= 32 ? 2 : R <= 64 ? 4 : 8; }
 
 int experts_down_splits(int64_t M, int64_t E, int64_t K, int R) {
-  const int64_t slots = (int64_t)(rank_blocks(R) <= 4 ? 2 : 1) * device_cus();
-  int64_t want = slots / most_tiles(M, E, sk::DT);  // one round
+  int64_t want = device_cus() / most_tiles(M, E, sk::DT);  // one round, a workgroup to a compute unit
   const int64_t most = cdiv(K, 512);
   if (want > most) want = most;
   if (want > 64) want = 64;
@@ -898,7 +898,7 @@ void launch_experts_prepare(const uint16_t* g, uint16_t* gout, const uint16_t* B
 // Sums the splits of u or v in order: fp32 out (may be null) and, for the
 // products over rows, bf16 hi and lo planes [M][16 RB] with zero ranks from R
 // on (planes may be null).  Rows outside every expert are left alone.  8192
-// rows of 16 ranks, 7 splits: 4-5 us, its launch and one trip to memory.
+// rows of 16 ranks, 3 splits: 4-5 us, its launch and one trip to memory.
 __global__ __launch_bounds__(256) void experts_factor_kernel(FactorJob a, FactorJob b, ExpertRows er, int R, int RP) {
   const FactorJob j = blockIdx.y ? b : a;
   const int i = (int)(blockIdx.x * 256 + threadIdx.x);  // rank pairs of all rows (fewer than 2^29)
@@ -955,7 +955,7 @@ void launch_experts_factor(const FactorJob* jobs, int count, const int32_t* offs
 // adds in order (it also writes the zeros of experts without rows; where no
 // expert can have two chunks, it is not needed).  Bound by the read of x and
 // g.  Both products in one launch, 8192 rows of 4096 and 14336 columns, r = 16:
-// 61 us and 5 us for the sums (302 MB, 4.6 TB/s); 4096 rows of 28672 and 8192
+// 56 us and 5 us for the sums (302 MB, 5.0 TB/s); 4096 rows of 28672 and 8192
 // columns, r = 64: 70 us and 8 us (3.9 TB/s).
 struct TokenJob {
   const uint16_t* X;   // M x ld
@@ -1174,13 +1174,13 @@ __global__ __launch_bounds__(256) void experts_sum_kernel(TokenArgs a) {
 // stage are as large as 128 columns of it, 8.
 static int token_waves(int R) { return rank_blocks(R) == 4 ? 8 : 4; }
 
-// Rows of a chunk: as many workgroups as run at once, if all experts had
-// whole chunks, but no fewer than 256 rows, below which the sums weigh as much
-// as the rows (4 x 8192 x 28672, 4096 rows, 64 ranks: 72 us and 10 us for the
-// sums; with chunks of a third 91 and 19 us).
+// Rows of a chunk: a workgroup to each compute unit, if all experts had whole
+// chunks, but no fewer than 256 rows, below which the sums weigh as much as
+// the rows.  4 x 8192 x 28672, 4096 rows, 64 ranks: 70 us and 8 us for the
+// sums, with chunks of half 81 and 15, of a third 91 and 17; 8 x 14336 x 4096,
+// 8192 rows, 16 ranks: 56 us, half 59, a third 58, 5 us for the sums each.
 static int token_chunk(int64_t M, int64_t J, int R) {
-  const int64_t want = (int64_t)(rank_blocks(R) <= 2 ? 2 : 1) * device_cus();
-  const int64_t c = cdiv(cdiv(M * cdiv(J, 32 * token_waves(R)), want), 64) * 64;
+  const int64_t c = cdiv(cdiv(M * cdiv(J, 32 * token_waves(R)), device_cus()), 64) * 64;
   return (int)(c < 256 ? 256 : c);
 }
 
