@@ -1209,13 +1209,16 @@ qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
   if (!aligned16(workspace)) return QLORA_ERR_ALIGN;
   hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
   float* const u = u_out ? u_out : at<float>(workspace, w.u);
-  float* const part = at<float>(workspace, w.part);
-  const bool streamed = experts_stream_takes(M, E, m, n);  // then u's splits are summed where they are used
+  // u's splits are summed where they are used, or by a launch of their own, or
+  // u is whole at once (64 x 512 x 1024, 200 rows an expert: 36 us, with that
+  // launch 41)
+  const bool streamed = experts_stream_takes(M, E, m, n), whole = !streamed && w.splits == 1;
+  float* const part = whole ? u : at<float>(workspace, w.part);
   {
     Timed tm("experts_down", hs);
     launch_experts_down(x, offsets, M, E, n, A, false, n, r, part, w.splits, hs);
     const FactorJob job{part, w.splits, u, nullptr};
-    if (!streamed) launch_experts_factor(&job, 1, offsets, M, E, r, hs);
+    if (!streamed && !whole) launch_experts_factor(&job, 1, offsets, M, E, r, hs);
   }
   {
     Timed tm("experts_fwd_gemm", hs);
