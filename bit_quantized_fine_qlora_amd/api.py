@@ -679,7 +679,7 @@ def _experts(x, offsets, q, A, B):
     _need(q.codes, torch.uint8, (cells // 2,), "q.codes")
     _need(q.absmax8, torch.uint8, (cells // 64,), "q.absmax8")
     _need(q.c2, torch.float32, (-(-cells // 16384),), "q.c2")
-    _same_device(x.device, offsets=offsets, A=A, B=B, q=q.codes)
+    _same_device(x.device, offsets=offsets, A=A, B=B, **{"q.codes": q.codes, "q.absmax8": q.absmax8, "q.c2": q.c2})
     return M, E, n, m, r
 
 
@@ -893,7 +893,8 @@ class AdamWStep:
     def run(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
             step: int = 1, clip: torch.Tensor | None = None) -> None:
         """One step (number `step`, from 1).  clip: what clip() returned, to multiply the gradients by its factor;
-        where that is NaN the step is not taken."""
+        where that is NaN the step is not taken.  lr, step and the others are values of this call: a graph that
+        captured it replays them."""
         if clip is not None:
             _need(clip, torch.float32, (2,), "clip")
             _same_device(self.device, clip=clip)

@@ -676,8 +676,9 @@ qlora_status qlora_grad_clip(const qlora_adamw_handle* handle, double max_norm, 
  * (clip: device, the output of qlora_grad_clip, or NULL for 1).  A factor
  * that is not finite takes no step: nothing is written.  8-bit moments are
  * formed in 64 bits and the weight's update reads them before their rounding.
- * Hyperparameters as there, eps at least 2^-126 in fp32.  With 8-bit moments
- * gradients must be finite (checked by a clip); fp32 moments as there.
+ * Hyperparameters as there, eps at least 2^-126 in fp32; a captured call
+ * replays them, step included.  With 8-bit moments gradients must be finite
+ * (checked by a clip); fp32 moments as there.
  */
 qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
                               double weight_decay, int64_t step, const float* clip, qlora_stream_t stream);
