@@ -794,6 +794,13 @@ def moment8_values(moment: Moment8, out: torch.Tensor | None = None) -> torch.Te
     return out
 
 
+# AdamWStep's tensors: name, dtype (None: either of the gradient's), bytes of an element (0: only read), one a block
+_PARAM = (("grad", None, 0, False), ("param", torch.float32, 4, False), ("param_bf16", torch.bfloat16, 2, False))
+_PARTS_F32 = (*_PARAM, ("exp_avg", torch.float32, 4, False), ("exp_avg_sq", torch.float32, 4, False))
+_PARTS_8BIT = (*_PARAM, ("exp_avg.codes", torch.uint8, 1, False), ("exp_avg.steps", torch.float32, 4, True),
+               ("exp_avg_sq.codes", torch.uint8, 1, False), ("exp_avg_sq.steps", torch.float32, 4, True))
+
+
 class AdamWStep:
     """Prepared optimizer step over any number of tensors, one launch a step.
 
@@ -812,7 +819,7 @@ class AdamWStep:
             device = torch.device(device)
             if device.index is None:
                 device = torch.device(device.type, torch.cuda.current_device())
-        index = -1 if device is None else device.index
+        index = -2 if device is None else device.index
         arr = (_lib.AdamWTensor * len(self._keep))()
         spans = []  # (first byte, end, tensor, written)
         for i, (p, p16, g, m, v) in enumerate(self._keep):
@@ -820,40 +827,40 @@ class AdamWStep:
             eight = isinstance(m, Moment8)
             if eight != isinstance(v, Moment8):
                 raise TypeError("exp_avg and exp_avg_sq: both Moment8 or neither")
-            named = [("grad", g, g.dtype, n), ("param", p, torch.float32, n)]
-            if p16 is not None:
-                named.append(("param_bf16", p16, torch.bfloat16, n))
-            if eight:
-                if not m.signed or v.signed:
-                    raise ValueError("exp_avg must be a signed Moment8, exp_avg_sq one that is not")
-                steps = -(-n // MOMENT_BLOCK)
-                named += [("exp_avg.codes", m.codes, torch.uint8, n), ("exp_avg.steps", m.steps, torch.float32, steps),
-                          ("exp_avg_sq.codes", v.codes, torch.uint8, n),
-                          ("exp_avg_sq.steps", v.steps, torch.float32, steps)]
-            else:
-                named += [("exp_avg", m, torch.float32, n), ("exp_avg_sq", v, torch.float32, n)]
+            steps = -(-n // MOMENT_BLOCK) if eight else 0
+            if eight and (not m.signed or v.signed):
+                raise ValueError("exp_avg must be a signed Moment8, exp_avg_sq one that is not")
             gtype = _type_of(g, "grad")
-            ptrs = []
-            for nm, t, dtype, count in named:
-                if t.dtype is not dtype:
-                    raise TypeError(f"{nm}: expected {dtype}, got {t.dtype}")
+            given = (g, p, p16, m.codes, m.steps, v.codes, v.steps) if eight else (g, p, p16, m, v)
+            ptrs, absent = [], None
+            for t, (name, dtype, size, per_block) in zip(given, _PARTS_8BIT if eight else _PARTS_F32):
+                if t is None and name == "param_bf16":
+                    ptrs.append(None)
+                    continue
+                count = steps if per_block else n
+                if t.dtype is not dtype and dtype is not None:
+                    raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
                 if t.numel() != count or not t.is_contiguous():
-                    raise ValueError(f"{nm}: expected {count} contiguous elements")
-            for nm, t, dtype, count in named:
+                    raise ValueError(f"{name}: expected {count} contiguous elements")
                 on = t.get_device()
-                if on < 0:
-                    if not t.is_pinned():
-                        raise ValueError(f"{nm}: must be on the GPU or in pinned host memory")
-                elif index < 0:
-                    index, device = on, t.device
-                elif on != index:
-                    raise ValueError(f"{nm}: all tensors must be on {device}, got one on {t.device}")
+                if on != index:
+                    if on < 0:
+                        if not t.is_pinned():
+                            absent = absent or name
+                    elif index < 0:
+                        index, device = on, t.device
+                    else:
+                        raise ValueError(f"{name}: all tensors must be on {device}, got one on {t.device}")
                 ptr = t.data_ptr()
-                spans.append((ptr, ptr + count * t.element_size(), i, nm != "grad"))
+                spans.append((ptr, ptr + count * (size or t.element_size()), i, size != 0))
                 ptrs.append(ptr)
-            at = 2 if p16 is None else 3  # the moments'
-            rest = (ptrs[at], ptrs[at + 2], ptrs[at + 1], ptrs[at + 3]) if eight else (*ptrs[at:], None, None)
-            arr[i] = (n, ptrs[1], None if p16 is None else ptrs[2], ptrs[0], *rest, gtype, int(eight))
+            if absent:
+                raise ValueError(f"{absent}: must be on the GPU or in pinned host memory")
+            if eight:
+                pg, pp, p16, pm, pms, pv, pvs = ptrs
+            else:
+                (pg, pp, p16, pm, pv), pms, pvs = ptrs, None, None
+            arr[i] = (n, pp, p16, pg, pm, pv, pms, pvs, gtype, int(eight))
         spans.sort()
         read, wrote = (0, 0), (0, 0)  # the furthest end so far, and whose it is
         for begin, end, i, writes in spans:
