@@ -63,9 +63,13 @@ __device__ __forceinline__ int wave_scan_add(int v) {
   return wave_scan(v, [](int a, int b) { return a + b; });
 }
 
-// 64 experts at a time, one a lane.  Offsets are held within 0 .. M and below
-// none before them, so that every row belongs to one expert at most whatever
-// they hold, and the tiles of all experts are as few as the host assumes.
+// 64 experts at a time, one a lane, the next 64 offsets on their way.  Offsets
+// are held within 0 .. M and below none before them, so that every row belongs
+// to one expert at most whatever they hold, and the tiles of all experts are as
+// few as the host assumes.  kMany: more than 64 experts (1024 x 4096 x 512,
+// 40000 rows: 1160 us; with a second pass over all offsets, and none on their
+// way, 1340.  One form for all numbers costs 64 x 1024 x 2048 1 us of 55).
+template <bool kMany>
 struct ExpertScan {
   int first = 0;               // expert of lane 0
   int end = 0;                 // last row + 1 of the experts before
@@ -73,18 +77,35 @@ struct ExpertScan {
   int row0 = 0, rows = 0, t = 0;  // of this lane's expert
   int t_incl = 0, s_incl = 0;     // with those of the lanes below
 
+  int ahead = 0;  // offset behind this lane's expert of the 64 that are loaded next
+  // Lane k: what comes before the experts from 64 k on (of those passed; 64
+  // lanes hold 4096 experts), so that a second look at any 64 is one step.
+  int k_end = 0, k_tiles = 0, k_slots = 0;
+
   __device__ __forceinline__ static int held(int v, int M) { return v < 0 ? 0 : v > M ? M : v; }
+  __device__ __forceinline__ void fetch(const ExpertRows& r, int from) {
+    const int e = from + (threadIdx.x & 63);
+    ahead = r.offsets[e < r.E ? e + 1 : r.E];
+  }
   __device__ __forceinline__ void begin(const ExpertRows& r) {
     first = tiles = slots = 0;
+    fetch(r, 0);
     end = held(r.offsets[0], r.M);
   }
   __device__ __forceinline__ void load(const ExpertRows& r, int bt) {
     const int lane = threadIdx.x & 63;
-    const int e = first + lane;
-    int last = held(r.offsets[e < r.E ? e + 1 : r.E], r.M);
+    int last = held(ahead, r.M);
+    if (kMany) {
+      if (first + 64 < r.E) fetch(r, first + 64);
+      if (lane == first >> 6) {
+        k_end = end;
+        k_tiles = tiles;
+        k_slots = slots;
+      }
+    }
     last = wave_scan_max(last > end ? last : end);
     row0 = __builtin_amdgcn_update_dpp(end, last, 0x138, 0xF, 0xF, false);  // wave_shr:1, `end` into lane 0
-    rows = e < r.E ? last - row0 : 0;
+    rows = first + lane < r.E ? last - row0 : 0;
     t = (rows + bt - 1) / bt;
     t_incl = wave_scan_add(t);
     s_incl = wave_scan_add(t > 1 ? t : 0);
@@ -94,6 +115,19 @@ struct ExpertScan {
     end = __builtin_amdgcn_readlane(row0 + rows, 63);
     tiles += __builtin_amdgcn_readlane(t_incl, 63);
     slots += __builtin_amdgcn_readlane(s_incl, 63);
+  }
+  // Back to the last of the 64s passed whose lane has `before` at most `want`.
+  __device__ __forceinline__ void again(const ExpertRows& r, int bt, int before, int want) {
+    const int lane = threadIdx.x & 63;
+    const int k = 63 - __builtin_clzll(__ballot(lane <= first >> 6 && before <= want));
+    if (k != first >> 6) {
+      first = 64 * k;
+      end = __builtin_amdgcn_readlane(k_end, k);
+      tiles = __builtin_amdgcn_readlane(k_tiles, k);
+      slots = __builtin_amdgcn_readlane(k_slots, k);
+      fetch(r, first);
+      load(r, bt);
+    }
   }
   __device__ __forceinline__ Span span(int lane, int tile) const {
     Span s;
@@ -109,54 +143,50 @@ struct ExpertScan {
 
 // The tile of bt rows that pick(number of tiles) names, found by every wave
 // for itself; false where pick names none.
-template <typename Pick>
-__device__ __forceinline__ bool find_span(const ExpertRows& r, int bt, Pick pick, Span& s) {
-  ExpertScan k;
+template <bool kMany, typename Pick>
+__device__ __forceinline__ bool find_span_of(const ExpertRows& r, int bt, Pick pick, Span& s) {
+  ExpertScan<kMany> k;
   k.begin(r);
   k.load(r, bt);
-  if (r.E > 64) {
-    while (k.first + 64 < r.E) {
-      k.next(r);
-      k.load(r, bt);
-    }
+  while (kMany && k.first + 64 < r.E) {
+    k.next(r);
+    k.load(r, bt);
   }
   const int total = k.tiles + __builtin_amdgcn_readlane(k.t_incl, 63);
   const int item = __builtin_amdgcn_readfirstlane(pick(total));
   if (item < 0 || item >= total) return false;
-  if (r.E > 64) {
-    k.begin(r);
-    k.load(r, bt);
-    while (k.tiles + __builtin_amdgcn_readlane(k.t_incl, 63) <= item) {
-      k.next(r);
-      k.load(r, bt);
-    }
-  }
+  if (kMany) k.again(r, bt, k.k_tiles, item);
   const uint64_t after = __ballot(k.tiles + k.t_incl > item);
   const int lane = __builtin_ctzll(after);
   const int before = k.tiles + __builtin_amdgcn_readlane(k.t_incl - k.t, lane);
   s = k.span(lane, item - before);
   return true;
 }
+template <typename Pick>
+__device__ __forceinline__ bool find_span(const ExpertRows& r, int bt, Pick pick, Span& s) {
+  return r.E > 64 ? find_span_of<true>(r, bt, pick, s) : find_span_of<false>(r, bt, pick, s);
+}
 
 // The same with the tiles numbered whole ones first and then each expert's
 // ragged last one: a launch then ends with its short tiles.  pick(whole,
 // ragged) names a tile of whole + ragged.
-template <typename Pick>
-__device__ __forceinline__ bool find_span_whole_first(const ExpertRows& r, int bt, Pick pick, Span& s) {
-  auto counts = [&](const ExpertScan& k, int& w, int& g) {  // of the lanes up to this one
+template <bool kMany, typename Pick>
+__device__ __forceinline__ bool find_whole_first_of(const ExpertRows& r, int bt, Pick pick, Span& s) {
+  auto counts = [&](const ExpertScan<kMany>& k, int& w, int& g) {  // of the lanes up to this one
     const int whole = k.rows / bt;
     g = __popcll(__ballot(k.t > whole) & (~0ull >> (63 - (threadIdx.x & 63))));
     w = k.t_incl - g;
   };
-  ExpertScan k;
+  ExpertScan<kMany> k;
   k.begin(r);
   k.load(r, bt);
-  int w, g, whole = 0, ragged = 0;
+  int w, g, whole = 0, ragged = 0, k_whole = 0;
   for (;;) {
+    if (kMany && (int)(threadIdx.x & 63) == k.first >> 6) k_whole = whole;
     counts(k, w, g);
     whole += __builtin_amdgcn_readlane(w, 63);
     ragged += __builtin_amdgcn_readlane(g, 63);
-    if (k.first + 64 >= r.E) break;
+    if (!kMany || k.first + 64 >= r.E) break;
     k.next(r);
     k.load(r, bt);
   }
@@ -164,28 +194,25 @@ __device__ __forceinline__ bool find_span_whole_first(const ExpertRows& r, int b
   if (item < 0 || item >= whole + ragged) return false;
   const bool last = item >= whole;
   int want = last ? item - whole : item;  // among the tiles of its kind
-  if (r.E > 64) {
-    k.begin(r);
-    k.load(r, bt);
+  if (kMany) {
+    const int before = last ? k.k_tiles - k_whole : k_whole;
+    k.again(r, bt, before, want);
+    want -= __builtin_amdgcn_readlane(before, k.first >> 6);
     counts(k, w, g);
-    for (;;) {
-      const int here = __builtin_amdgcn_readlane(last ? g : w, 63);
-      if (want < here) break;
-      want -= here;
-      k.next(r);
-      k.load(r, bt);
-      counts(k, w, g);
-    }
   }
   const int lane = __builtin_ctzll(__ballot((last ? g : w) > want));
   const int full = __builtin_amdgcn_readlane(k.rows / bt, lane);
   s = k.span(lane, last ? full : want - (__builtin_amdgcn_readlane(w, lane) - full));
   return true;
 }
+template <typename Pick>
+__device__ __forceinline__ bool find_span_whole_first(const ExpertRows& r, int bt, Pick pick, Span& s) {
+  return r.E > 64 ? find_whole_first_of<true>(r, bt, pick, s) : find_whole_first_of<false>(r, bt, pick, s);
+}
 
 // Expert e's rows and tiles (its first).
 __device__ __forceinline__ Span expert_span(const ExpertRows& r, int bt, int e) {
-  ExpertScan k;
+  ExpertScan<true> k;
   k.begin(r);
   k.load(r, bt);
   while (e >= k.first + 64) {
@@ -209,7 +236,7 @@ __device__ __forceinline__ void live_rows(const ExpertRows& r, int& low, int& to
     top = o > top ? o : top;
   }
   top = top < r.M ? top : r.M;
-  low = ExpertScan::held(r.offsets[0], r.M);
+  low = ExpertScan<false>::held(r.offsets[0], r.M);
 }
 
 // Most tiles of bt rows that M rows of E experts make.
