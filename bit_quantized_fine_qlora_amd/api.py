@@ -806,7 +806,7 @@ class AdamWStep:
 
     tensors: list of (param fp32, param_bf16 bf16 or None, grad bf16 or fp32, exp_avg, exp_avg_sq), the moments
     both fp32 tensors or both Moment8 (signed first); each contiguous with the same number of elements, on one GPU
-    or (the gradient too) in pinned host memory.  The tensors' table is written to `device` (the GPU of the
+    or (the gradient too) in pinned host memory.  The tensors' table is written to `device` (a GPU: that of the
     tensors, or the current one) here, on the current stream; the tensors must stay where they are.  clip() and
     run() of one AdamWStep must be ordered.
     """
@@ -817,8 +817,10 @@ class AdamWStep:
             raise ValueError("no tensors")
         if device is not None:
             device = torch.device(device)
+            if device.type != "cuda":  # the table's own place: a kernel writes it, also for tensors in host memory
+                raise ValueError(f"device: must be a GPU, got {device}")
             if device.index is None:
-                device = torch.device(device.type, torch.cuda.current_device())
+                device = torch.device("cuda", torch.cuda.current_device())
         index = -2 if device is None else device.index
         arr = (_lib.AdamWTensor * len(self._keep))()
         spans = []  # (first byte, end, tensor, written)
