@@ -72,7 +72,7 @@ BF16_PEAK_TFLOPS = 2500.0
 # plus one fp32 half-sum per tile.
 GEMM_SRC = [os.path.join(ROOT, "bit_quantized_fine_qlora_amd", "csrc", f) for f in ("gemm_linear.hip", "gemm_tile.h", "qlora_common.h")]
 GEMM_TRAFFIC = {
-    "src_sha1": "fa5878e09ac013d9d2abbce6643f71cf80ec8fb5",
+    "src_sha1": "3bd7c8b3726f4ca84836aa2af78c322da2ea0f30",
     "q/fwd_gemm": {"fetch": 1297956352, "write": 134244224},
     "k/fwd_gemm": {"fetch": 584374315, "write": 50344448},
     "v/fwd_gemm": {"fetch": 584374699, "write": 50345301},

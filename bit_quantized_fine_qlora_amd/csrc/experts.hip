@@ -276,7 +276,7 @@ __device__ __forceinline__ int pieces_of(int tiles, int slots, int nk) {
   return p > 1 ? p : 1;
 }
 
-template <bool kBwd, bool kPieces>
+template <bool kBwd, bool kPieces, bool kTail = false>
 __global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p, ExpertRows er, Nf4Table tab,
                                                                      int slots) {
   using T = lg2::Tile<kBwd>;
@@ -341,13 +341,13 @@ __global__ __launch_bounds__(lg2::kThreads) void experts_gemm_kernel(GemmArgs p,
   if (tid >= 64 * lg2::kMfmaWaves)
     gemm_producer<kBwd>(p, tab, lds, tid - 64 * lg2::kMfmaWaves, f0, t0, k0, ks, lora, 0, &lds_word, skew);
   else if (left > 192)
-    gemm_consumer<kBwd, kPieces, false, lg2::BT, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, lg2::BT, true, kTail>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else if (left > 128)
-    gemm_consumer<kBwd, kPieces, false, 192, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 192, true, kTail>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else if (left > 64)
-    gemm_consumer<kBwd, kPieces, false, 128, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 128, true, kTail>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
   else
-    gemm_consumer<kBwd, kPieces, false, 64, true>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
+    gemm_consumer<kBwd, kPieces, false, 64, true, kTail>(p, lds, tid, f0, t0, k0, ks, lora, 0, &lds_word);
 }
 
 // Finishes tiles that ran as K pieces: out = bf16(piece 0 + piece 1 + ...), in
@@ -443,8 +443,11 @@ void launch_experts_gemm(bool bwd, const int32_t* offsets, int64_t E, const uint
   // the runs of whole and of ragged tiles are each rounded up to 8
   const int64_t wgs = cdiv(tiles, 8) * 8 + 8;
   const dim3 grid((unsigned)wgs);
+  const bool tail = K % lg2::BK != 0;  // of the backward only: n is a multiple of 64
   if (!slots || 2 * tiles > slots) {
-    if (bwd)
+    if (tail)
+      hipLaunchKernelGGL((experts_gemm_kernel<true, false, true>), grid, block, 0, stream, p, er, tab, slots);
+    else if (bwd)
       hipLaunchKernelGGL((experts_gemm_kernel<true, false>), grid, block, 0, stream, p, er, tab, slots);
     else
       hipLaunchKernelGGL((experts_gemm_kernel<false, false>), grid, block, 0, stream, p, er, tab, slots);
@@ -455,7 +458,10 @@ void launch_experts_gemm(bool bwd, const int32_t* offsets, int64_t E, const uint
   const dim3 pgrid((unsigned)pieces_items(M, E, p.N, K));
   const dim3 rgrid((unsigned)((tiles < slots / 2 ? tiles : slots / 2) * (lg2::BF * lg2::BT / 4 / 256)));
   if (bwd) {
-    hipLaunchKernelGGL((experts_gemm_kernel<true, true>), pgrid, block, 0, stream, p, er, tab, slots);
+    if (tail)
+      hipLaunchKernelGGL((experts_gemm_kernel<true, true, true>), pgrid, block, 0, stream, p, er, tab, slots);
+    else
+      hipLaunchKernelGGL((experts_gemm_kernel<true, true>), pgrid, block, 0, stream, p, er, tab, slots);
     hipLaunchKernelGGL(experts_pieces_kernel<true>, rgrid, dim3(256), 0, stream, p, er, slots);
   } else {
     hipLaunchKernelGGL((experts_gemm_kernel<false, true>), pgrid, block, 0, stream, p, er, tab, slots);

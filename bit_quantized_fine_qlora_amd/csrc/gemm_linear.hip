@@ -8,8 +8,9 @@
 namespace qlora {
 
 // kPieces: few-tile mode (every tile as p.pieces K pieces), a separate
-// instantiation so that the other kernels' register allocation is untouched.
-template <bool kBwd, bool kPieces, bool kSkip>
+// instantiation so that the other kernels' register allocation is untouched;
+// kTail (K not a multiple of 64) likewise.
+template <bool kBwd, bool kPieces, bool kSkip, bool kTail = false>
 __global__ __launch_bounds__(lg2::kThreads) void linear_gemm_kernel(GemmArgs p, Nf4Table tab) {
   using T = lg2::Tile<kBwd>;
   __shared__ __align__(16) uint8_t sw0[T::W];
@@ -49,7 +50,7 @@ __global__ __launch_bounds__(lg2::kThreads) void linear_gemm_kernel(GemmArgs p, 
   if (tid >= 64 * lg2::kMfmaWaves)
     gemm_producer<kBwd>(p, tab, lds, tid - 64 * lg2::kMfmaWaves, f0, t0, k0, ks, lora, split, &lds_word);
   else
-    gemm_consumer<kBwd, kPieces, kSkip>(p, lds, tid, f0, t0, k0, ks, lora, split, &lds_word);
+    gemm_consumer<kBwd, kPieces, kSkip, lg2::BT, false, kTail>(p, lds, tid, f0, t0, k0, ks, lora, split, &lds_word);
 }
 
 __global__ void zero_u32_kernel(uint32_t* p, int n) {
@@ -183,7 +184,12 @@ template <bool kPieces>
 static void launch_gemm_kernel(bool bwd, bool skip, dim3 grid, const GemmArgs& p, const Nf4Table& tab,
                                hipStream_t stream) {
   const dim3 block(lg2::kThreads);
-  if (bwd) {
+  if (bwd && p.K % lg2::BK != 0) {
+    if (skip)
+      hipLaunchKernelGGL((linear_gemm_kernel<true, kPieces, true, true>), grid, block, 0, stream, p, tab);
+    else
+      hipLaunchKernelGGL((linear_gemm_kernel<true, kPieces, false, true>), grid, block, 0, stream, p, tab);
+  } else if (bwd) {
     if (skip)
       hipLaunchKernelGGL((linear_gemm_kernel<true, kPieces, true>), grid, block, 0, stream, p, tab);
     else

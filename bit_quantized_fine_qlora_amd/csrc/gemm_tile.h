@@ -141,7 +141,7 @@ __device__ __forceinline__ void gemm_producer(const GemmArgs& p, const Nf4Table&
   // past m / n of W0) read zeros or other rows of the same tensor; they only
   // feed outputs that are never stored.  In the backward's last K step the
   // W0 rows past m read zero codes and a zero 8-bit constant, i.e. zero
-  // weights, so the finite activations there add nothing.
+  // weights, and the activations there read zero too (kTail below).
   const brsrc_t r_codes = make_rsrc(p.codes, (uint32_t)(wnumel / 2));
   const brsrc_t r_amax = make_rsrc(p.absmax8, (uint32_t)(wnumel / kBlock));
   const brsrc_t r_c2 =
@@ -338,8 +338,11 @@ struct WaveTile {
 
 // MFMA waves (512 threads): each owns a WF-feature x WT-token output tile.
 // kRows: tokens that the tile covers at most, 256, 192, 128 or 64.  kPlain: the
-// tile is never split in two halves and nothing is added to it.
-template <bool kBwd, bool kPieces, bool kSkip, int kRows = lg2::BT, bool kPlain = false>
+// tile is never split in two halves and nothing is added to it.  kTail: K is
+// not a multiple of 64 (of 8 it is), and the last K step's columns from K on,
+// which lie in the token's next row, read as zero: their weights are zero, but
+// 0 times an infinity or NaN of another token is NaN.
+template <bool kBwd, bool kPieces, bool kSkip, int kRows = lg2::BT, bool kPlain = false, bool kTail = false>
 __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds& lds, int tid, int64_t f0,
                                               int64_t t0, int k0, int nk, bool lora, int split, uint32_t* lds_word) {
   constexpr int WF = WaveTile<kBwd, kRows>::F;
@@ -383,6 +386,17 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (__attribute__((address_space(3))) void*)(dst + 1024 * b), 16,
                                                act_off + act_blk * b, 0, 0, 0);
     act_off += lg2::BK * 2;
+  };
+  // kTail, before the copy of K step ks: where K ends in it, the columns from
+  // there on are read out of range.  A token's offsets lie below 2^31, the
+  // buffer ends there, and with the top bit set the offsets of all its blocks
+  // still lie below 2^32.  The branch is the wave's and taken once (8192 x 4096
+  // x 8200: 2 % of the call; a comparison a lane in every step 4 %).
+  const int cut = kTail ? (int)(p.K / lg2::BK) - k0 : 0;
+  auto cut_act = [&](int ks) {
+    if constexpr (kTail)
+      if (__builtin_expect(ks == cut, 0))
+        act_off |= 8 * ((lane & 7) ^ (lane >> 3)) >= (int)(p.K % lg2::BK) ? 0x80000000u : 0u;
   };
 
   // Fragment addresses: one per-lane base plus immediate offsets.
@@ -461,7 +475,10 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
   // K step ks on stage (w, a) while the next activation tile goes to a_next
   const bool lora16 = !kBwd && p.r <= 16;  // a LoRA step then fills only its first K half
   auto step = [&](int ks, const uint8_t* w, const uint8_t* a, uint8_t* a_next) {
-    if (ks + 1 < nk) copy_act(a_next);
+    if (ks + 1 < nk) {
+      cut_act(ks + 1);
+      copy_act(a_next);
+    }
     if (active) {
       mfma_step(w, a, 0);
       if (!(lora16 && ks >= nk)) mfma_step(w, a, 1);
@@ -471,6 +488,7 @@ __device__ __forceinline__ void gemm_consumer(const GemmArgs& p, const lg2::Lds&
   };
   // nk steps of W' and activations, then the LoRA steps (filled by the producers)
   const int nsteps = nk + (lora ? (p.r + 31) / 32 : 0);
+  cut_act(0);
   copy_act(lds.a[0]);
   __builtin_amdgcn_s_waitcnt(kWaitVm0);
   __syncthreads();  // stage 0 ready
