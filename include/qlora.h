@@ -676,6 +676,8 @@ qlora_status qlora_grad_clip(const qlora_adamw_handle* handle, double max_norm, 
  * (clip: device, the output of qlora_grad_clip, or NULL for 1).  A factor
  * that is not finite takes no step: nothing is written.  8-bit moments are
  * formed in 64 bits and the weight's update reads them before their rounding.
+ * lr weight_decay p and the update are added and then taken from p in one
+ * rounding, so that a decay below fp32's steps is right in the mean.
  * Hyperparameters as there, eps at least 2^-126 in fp32; a captured call
  * replays them, step included.  With 8-bit moments gradients must be finite
  * (checked by a clip); fp32 moments as there.
