@@ -270,7 +270,17 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
     dm = dm < kTiny ? 0.0f : dm;
     dv = dv < kTiny ? 0.0f : dv;
     const float im = dm > 0.0f ? 1.0f / dm : 0.0f;
-    const double iv = dv > 0.0f ? 1.0 / ((double)dv * (double)dv) : 0.0;
+    // Roots are taken in fp32 as parts of the block's largest, of squares scaled
+    // to 2^126 at most, so that neither a small block nor a small element beside
+    // a large one leaves fp32's range (down to 2^-126 of the largest); where the
+    // largest is past 2^125, whose reciprocals are not normal numbers, the
+    // quotient's parts are scaled too.
+    const float big = (float)__builtin_sqrt(vtop);
+    const double iv = vtop > 0.0 ? 0x1p126 / vtop : 0.0;
+    const float to_code = dv > 0.0f ? big / dv : 0.0f;
+    const float sc = big * c.inv_root_bc2 > 0x1p125f ? 0.25f : 1.0f;
+    const float to_denom = big * c.inv_root_bc2 * sc, eps = __builtin_fmaxf(c.eps * sc, 0x1p-126f);
+    const float step_size = c.step_size * sc;
     u32x2 mo = {0u, 0u}, vo = {0u, 0u};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -281,8 +291,8 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
       uint32_t mc = (uint32_t)__builtin_fminf(k, 127.0f);
       mc = dm > 0.0f ? mc : 0u;
       mc |= (m[j] < 0.0 && mc) ? 128u : 0u;
-      const float root = __builtin_amdgcn_sqrtf((float)(v[j] * iv));  // sqrt(v) / d
-      k = root_floor(root);
+      const float root = __builtin_amdgcn_sqrtf((float)(v[j] * iv)) * 0x1p-63f;
+      k = root_floor(root * to_code);
       const double border = (double)(k * k + k + 0.5f) * (double)dv;
       k += v[j] > border * border ? 1.0f : 0.0f;
       uint32_t vc = (uint32_t)__builtin_fminf(k, 255.0f);
@@ -290,8 +300,8 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
       vc = dv > 0.0f ? vc : 0u;
       mo[j >> 2] |= mc << (8 * (j & 3));
       vo[j >> 2] |= vc << (8 * (j & 3));
-      const float denom = root * dv * c.inv_root_bc2 + c.eps;
-      const float u = c.step_size * ((m[j] < 0.0 ? -mf : mf) * __builtin_amdgcn_rcpf(denom));
+      const float denom = __builtin_fmaf(root, to_denom, eps);
+      const float u = step_size * ((m[j] < 0.0 ? -mf : mf) * __builtin_amdgcn_rcpf(denom));
       p[j] -= __builtin_fmaf(c.decay, p[j], u);
     }
     if (left <= 0 || !(__builtin_fabsf(factor) < __builtin_inff())) return;
