@@ -111,6 +111,8 @@ PROTOTYPES = {
     "qlora_grad_clip": (ctypes.c_int, [ctypes.POINTER(AdamWHandle), c_f64, c_vp, c_vp]),
     "qlora_adamw_step": (ctypes.c_int, [ctypes.POINTER(AdamWHandle), c_f64, c_f64, c_f64, c_f64, c_f64, c_i64, c_vp,
                                         c_vp]),
+    "qlora_adamw_step_ex": (ctypes.c_int, [ctypes.POINTER(AdamWHandle), c_f64, c_f64, c_f64, c_f64, c_f64, c_i64, c_vp,
+                                           ctypes.POINTER(ctypes.c_uint64), c_vp]),
     "qlora_moment8_values": (ctypes.c_int, [c_i32, c_i64, c_vp, c_vp, c_vp, c_vp]),
     "qlora_linear_check": (ctypes.c_int, [ctypes.c_int, c_i64, c_i64, c_i64, c_i32, c_vp, c_vp]),
     "qlora_profile_enable": (ctypes.c_int, [ctypes.c_int]),

@@ -260,6 +260,11 @@ def _workspace(op, M, n, m, r, device, workspace):
     return _room(workspace_bytes(op, M, n, m, r), device, workspace)
 
 
+def _seed(seed):
+    """An integer or None -> a pointer to its lower 64 bits or None."""
+    return None if seed is None else ctypes.pointer(ctypes.c_uint64(int(seed) & (2 ** 64 - 1)))
+
+
 def _dropout(dropout):
     """(p, seed, offset) or None -> a qlora_dropout pointer (None: plain layer)."""
     if dropout is None:
@@ -900,17 +905,19 @@ class AdamWStep:
         return out
 
     def run(self, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
-            step: int = 1, clip: torch.Tensor | None = None) -> None:
+            step: int = 1, clip: torch.Tensor | None = None, seed: int | None = None) -> None:
         """One step (number `step`, from 1).  clip: what clip() returned, to multiply the gradients by its factor;
-        where that is NaN the step is not taken.  lr, step and the others are values of this call: a graph that
-        captured it replays them."""
+        where that is NaN the step is not taken.  seed: second moments in 8 bits take one of the two codes about
+        their value, drawn from (seed, step) so that the mean is the value; None: the nearest, with which their
+        running average stops, for a few steps at most.  32-bit moments take no notice of it.  lr, step, seed and
+        the others are values of this call: a graph that captured it replays them."""
         if clip is not None:
             _need(clip, torch.float32, (2,), "clip")
             _same_device(self.device, clip=clip)
         with _on(self.device):
-            st = _lib.load().qlora_adamw_step(ctypes.byref(self._handle), float(lr), float(beta1), float(beta2),
-                                              float(eps), float(weight_decay), int(step), _ptr(clip),
-                                              _stream(self.device))
+            st = _lib.load().qlora_adamw_step_ex(ctypes.byref(self._handle), float(lr), float(beta1), float(beta2),
+                                                 float(eps), float(weight_decay), int(step), _ptr(clip),
+                                                 _seed(seed), _stream(self.device))
         _lib.check(st, "qlora_adamw_step")
 
 

@@ -26,7 +26,8 @@ constexpr int kPlanPerLaunch = 40;  // table entries in one launch's arguments (
 void launch_adamw_plan(const AdamWTensor* ts, int64_t first, int count, int64_t tensors, int64_t chunks, void* plan,
                        hipStream_t stream);
 void launch_adamw_step(void* plan, int64_t tensors, int64_t chunks, double lr, double beta1, double beta2, double eps,
-                       double weight_decay, int64_t step, const float* clip, hipStream_t stream);
+                       double weight_decay, int64_t step, const float* clip, const uint64_t* seed,
+                       hipStream_t stream);
 void launch_grad_clip(void* plan, int64_t tensors, int64_t chunks, double max_norm, float* out, hipStream_t stream);
 void launch_moment8_values(int is_signed, int64_t count, const uint8_t* codes, const float* steps, float* out,
                            hipStream_t stream);

@@ -20,7 +20,12 @@
 //      d = fp32(max root / 255^2); a v that is not 0 takes no k below 1, so
 //      that no element divides its first moment by eps alone
 // d below 2^-126 counts as 0 (the whole block is 0).  Each value takes the
-// nearest of them, the lower of two as near.  The new moments and that choice
+// nearest of them, the lower of two as near, or (kDrawn, v only) one of the two
+// about it, drawn so that the mean is the value.  Nearest codes stop v's running
+// average: a step moves it by 1 - b2 of itself, 0.1 %, and neighbours are 4 / k,
+// 1.6 % at least, apart, so a root whose gradients fall to a fifth beside others
+// that do not stays where it was (3.9 times too large 4000 steps later; drawn
+// codes 0.99 times).  m moves by 10 % a step and takes the nearest.  The new moments and that choice
 // are formed in 64 bits: what a code is then depends on the operands alone
 // and not on an order of fp32 operations, and fp64 multiplies and adds run at
 // the fp32 rate here.  The weight's update reads the moments before their
@@ -204,6 +209,12 @@ __device__ __forceinline__ double row_max(double v) {
 // exact comparison with k^2 + k + 1/2 (16 bits and a half) settles which.
 __device__ __forceinline__ float root_floor(float x) { return __builtin_floorf(__builtin_amdgcn_sqrtf(x)); }
 
+// The value of code k of a second moment with step d.
+__device__ __forceinline__ double root_code(float k, double d) {
+  const double root = (double)(k * k) * d;
+  return root * root;
+}
+
 struct AdamWConst {
   double b1, c1, b2, c2;  // beta, 1 - beta
   float f1, g1, f2, g2;   // the same in fp32
@@ -214,8 +225,13 @@ struct AdamWConst {
   float eps;
 };
 
+// kDrawn: element 2048 c + i of the plan (chunk c) takes word i % 4 of
+// Philox4x32-10 at the 64-bit counter 2^33 step + 512 c + i / 4 under the seed:
+// 2 calls for a thread's 8 elements.
+template <bool kDrawn>
 __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t tensors, AdamWConst c,
-                                                         const float* __restrict__ clip) {
+                                                         const float* __restrict__ clip, uint64_t seed,
+                                                         uint64_t counter) {
   const PlanView pv = plan_view(plan, tensors);
   // Read first and tested last, so that its latency is not added to the others'.
   // Not finite: gradients without a finite norm, no step.
@@ -274,14 +290,20 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
     // to 2^126 at most, so that neither a small block nor a small element beside
     // a large one leaves fp32's range (down to 2^-126 of the largest); where the
     // largest is past 2^125, whose reciprocals are not normal numbers, the
-    // quotient's parts are scaled too.
+    // quotient's parts are scaled too.  (The largest is 255^2 steps.)
     const float big = (float)__builtin_sqrt(vtop);
     const double iv = vtop > 0.0 ? 0x1p126 / vtop : 0.0;
-    const float to_code = dv > 0.0f ? big / dv : 0.0f;
     const float sc = big * c.inv_root_bc2 > 0x1p125f ? 0.25f : 1.0f;
     const float to_denom = big * c.inv_root_bc2 * sc, eps = __builtin_fmaxf(c.eps * sc, 0x1p-126f);
     const float step_size = c.step_size * sc;
     u32x2 mo = {0u, 0u}, vo = {0u, 0u};
+    u32x4 draw[2] = {};
+    if constexpr (kDrawn) {
+      const uint64_t at = counter + (uint64_t)blockIdx.x * (kChunk / 4) + 2 * threadIdx.x;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        draw[i] = philox4x32_10((uint32_t)(at + i), (uint32_t)((at + i) >> 32), (uint32_t)seed, (uint32_t)(seed >> 32));
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const double am = __builtin_fabs(m[j]);
@@ -292,9 +314,20 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
       mc = dm > 0.0f ? mc : 0u;
       mc |= (m[j] < 0.0 && mc) ? 128u : 0u;
       const float root = __builtin_amdgcn_sqrtf((float)(v[j] * iv)) * 0x1p-63f;
-      k = root_floor(root * to_code);
-      const double border = (double)(k * k + k + 0.5f) * (double)dv;
-      k += v[j] > border * border ? 1.0f : 0.0f;
+      if constexpr (kDrawn) {
+        k = root_floor(root * (255.0f * 255.0f));
+        // Next to a code (1e-4 of the way to the next at most, at k = 255) k may be
+        // one off either way: v then takes that code whatever the word, which moves
+        // the mean by less than 1e-8 of the way.  (With k put right 160-166 us
+        // instead of 152 for 41.9 million elements.)
+        const double lo = root_code(k, (double)dv), hi = root_code(k + 1.0f, (double)dv);
+        const double part = ((double)draw[j >> 2][j & 3] + 0.5) * 0x1p-32;
+        k += v[j] - lo > (hi - lo) * part ? 1.0f : 0.0f;
+      } else {
+        k = root_floor(root * (255.0f * 255.0f));
+        const double border = (double)(k * k + k + 0.5f) * (double)dv;
+        k += v[j] > border * border ? 1.0f : 0.0f;
+      }
       uint32_t vc = (uint32_t)__builtin_fminf(k, 255.0f);
       vc = vc == 0u && v[j] > 0.0 ? 1u : vc;
       vc = dv > 0.0f ? vc : 0u;
@@ -326,7 +359,8 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
 }
 
 void launch_adamw_step(void* plan, int64_t tensors, int64_t chunks, double lr, double beta1, double beta2, double eps,
-                       double weight_decay, int64_t step, const float* clip, hipStream_t stream) {
+                       double weight_decay, int64_t step, const float* clip, const uint64_t* seed,
+                       hipStream_t stream) {
   AdamWConst c;
   const double bc1 = 1.0 - std::pow(beta1, (double)step), bc2 = 1.0 - std::pow(beta2, (double)step);
   c.b1 = beta1;
@@ -342,7 +376,12 @@ void launch_adamw_step(void* plan, int64_t tensors, int64_t chunks, double lr, d
   c.inv_bc2 = (float)(1.0 / bc2);
   c.inv_root_bc2 = (float)std::sqrt(1.0 / bc2);
   c.eps = (float)eps;
-  hipLaunchKernelGGL(adamw_step_kernel, dim3((unsigned)chunks), dim3(256), 0, stream, plan, tensors, c, clip);
+  const dim3 grid((unsigned)chunks), block(256);
+  if (seed)
+    hipLaunchKernelGGL(adamw_step_kernel<true>, grid, block, 0, stream, plan, tensors, c, clip, *seed,
+                       (uint64_t)step << 33);
+  else
+    hipLaunchKernelGGL(adamw_step_kernel<false>, grid, block, 0, stream, plan, tensors, c, clip, 0ull, 0ull);
 }
 
 // ---------------------------------------------------------------------------

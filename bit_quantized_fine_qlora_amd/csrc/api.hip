@@ -1328,8 +1328,9 @@ qlora_status qlora_grad_clip(const qlora_adamw_handle* handle, double max_norm, 
   return hip_status();
 }
 
-qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
-                              double weight_decay, int64_t step, const float* clip, qlora_stream_t stream) {
+qlora_status qlora_adamw_step_ex(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
+                                 double weight_decay, int64_t step, const float* clip, const uint64_t* seed,
+                                 qlora_stream_t stream) {
   const qlora_status st = check_adamw_handle(handle);
   if (st != QLORA_OK) return st;
   if (step < 1 || !std::isfinite(lr) || lr < 0.0 || !std::isfinite(eps) || (float)eps < 1.17549435e-38f ||
@@ -1341,9 +1342,14 @@ qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, doubl
   {
     Timed tm("adamw", hs);
     launch_adamw_step(handle->plan, handle->tensors, handle->chunks, lr, beta1, beta2, eps, weight_decay, step, clip,
-                      hs);
+                      seed, hs);
   }
   return hip_status();
+}
+
+qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
+                              double weight_decay, int64_t step, const float* clip, qlora_stream_t stream) {
+  return qlora_adamw_step_ex(handle, lr, beta1, beta2, eps, weight_decay, step, clip, nullptr, stream);
 }
 
 qlora_status qlora_moment8_values(int32_t second, int64_t count, const uint8_t* codes, const float* steps, float* out,

@@ -22,7 +22,7 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import bit_quantized_fine_qlora_amd as Q  # noqa: E402
 
 TOKENS, WIDTH, INNER, EXPERTS, CHOSEN, RANK, SCALE = 200, 256, 512, 6, 2, 16, 1.0
-LR, MAX_NORM = 2e-3, 0.5
+LR, MAX_NORM, SEED = 2e-3, 0.5, 0  # SEED: of the second moments' codes, a step at a time
 
 
 class Trained:
@@ -107,7 +107,7 @@ def train_step(model, x, target, step):
     loss, grad = loss_of(out, target)
     backward(model, kept, grad)
     clip = model["optimizer"].clip(MAX_NORM)
-    model["optimizer"].run(LR, weight_decay=0.01, step=step, clip=clip)
+    model["optimizer"].run(LR, weight_decay=0.01, step=step, clip=clip, seed=SEED)
     return loss, clip[0]
 
 

@@ -624,8 +624,9 @@ qlora_status qlora_experts_bwd(int64_t M, int64_t E, int64_t n, int64_t m, int32
  * the sign, k = bits 0-6, the value +-k^2 d with d = fp32(largest / 127^2).
  * exp_avg_sq: its root is k^2 d, k = 0 .. 255, the value that squared, d =
  * fp32(largest root / 255^2); a value that is not 0 takes k >= 1.  Each value
- * takes the nearest of them, of two as near the lower, decided in 64 bits; a d
- * below 2^-126 is 0, and all of its block.
+ * takes the nearest of them, of two as near the lower, decided in 64 bits (an
+ * exp_avg_sq with a seed: see qlora_adamw_step_ex); a d below 2^-126 is 0, and
+ * all of its block.
  * Every pointer 16-byte aligned, but for the steps, which are read one by one
  * (4 bytes: the tensors may be slices of one storage, each from a block's
  * border on); tensors must not overlap.
@@ -684,6 +685,28 @@ qlora_status qlora_grad_clip(const qlora_adamw_handle* handle, double max_norm, 
  */
 qlora_status qlora_adamw_step(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
                               double weight_decay, int64_t step, const float* clip, qlora_stream_t stream);
+
+/*
+ * The same with drawn codes for 8-bit second moments (seed: host, 8 bytes read
+ * before the call returns; NULL: exactly qlora_adamw_step).  A training run of
+ * more than some ten steps with 8-bit moments wants them: the nearest codes
+ * keep a second moment where it is while its gradients change, since a step
+ * moves it by 1 - beta2 of itself, far less than codes lie apart.  (Measured, beta2 =
+ * 0.999: gradients of half of a block fall to a fifth, 4000 steps later their
+ * exp_avg_sq has 3.9 times the root that it should have, and drawn 0.99 times.)
+ * With a seed a value v between the neighbours a < b takes b with the
+ * probability (v - a) / (b - a), so that its mean is v; a v that is not 0 still
+ * takes no code below 1, and none above 255.  b is taken where v - a >
+ * (b - a) (w + 1/2) / 2^32 with w word i % 4 of Philox4x32-10 (as for
+ * qlora_dropout) at the 64-bit counter 2^33 step + 512 c + i / 4, for element i
+ * of the plan's chunk c of 2048 (within 1e-4 of the way from one code to the
+ * other v may take the code that it is next to whatever w): the same seed, step
+ * and plan give the same bits.  A captured call replays its draws, with which a moment that changes
+ * little stops as with the nearest codes: capture it anew, or keep 32 bits.
+ */
+qlora_status qlora_adamw_step_ex(const qlora_adamw_handle* handle, double lr, double beta1, double beta2, double eps,
+                                 double weight_decay, int64_t step, const float* clip, const uint64_t* seed,
+                                 qlora_stream_t stream);
 
 /*
  * The fp32 values that an 8-bit moment's `count` codes stand for; second: 0

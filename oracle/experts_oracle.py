@@ -4,6 +4,7 @@ float64 throughout; shares no code with the library.
 
   experts_fwd / experts_bwd   the adapted layer over the rows of many experts
   moment8_values / moment8_pack   moments in 8 bits
+  moment8_draws / moment8_pack_drawn   second moments in 8 bits with drawn codes
   grad_clip                   norm of all gradients and the factor that holds it to a maximum
   adamw_step                  the step of one tensor, moments given and returned in float64
 """
@@ -79,6 +80,35 @@ def moment8_pack(values, signed: bool):
         else:
             k = np.where((values[sl] > 0) & (k == 0), 1, k)
         codes[sl] = k
+    return codes, steps
+
+
+def moment8_draws(seed: int, step: int, chunk: int, count: int):
+    """The random words of a tensor of `count` elements that begins at chunk `chunk` of its plan."""
+    group = (step * 2 ** 33 + 512 * chunk + np.arange(-(-count // 4)).astype(object)) % 2 ** 64
+    group = group.astype(np.uint64)
+    words = O.philox4x32_10_np(group & np.uint64(0xFFFFFFFF), group >> np.uint64(32),
+                               (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF))
+    return np.stack(words, axis=1).reshape(-1)[:count]
+
+
+def moment8_pack_drawn(values, words):
+    """(codes, steps) of a second moment: of the two codes about a value the one that its word picks."""
+    values = np.asarray(values, dtype=np.float64)
+    codes = np.zeros(values.size, dtype=np.uint8)
+    steps = np.zeros(-(-values.size // MOMENT_BLOCK), dtype=np.float32)
+    for b in range(steps.size):
+        sl = slice(MOMENT_BLOCK * b, min(values.size, MOMENT_BLOCK * (b + 1)))
+        v = values[sl]
+        d = np.float32(np.sqrt(v.max()) / 255 ** 2)
+        if d < np.float32(2.0 ** -126):
+            continue
+        steps[b] = d
+        table = (np.arange(258, dtype=np.float64) ** 2 * float(d)) ** 2
+        k = np.searchsorted(table, v, side="right") - 1
+        a, up = table[k], table[k + 1]
+        k = k + (v - a > (up - a) * ((words[sl].astype(np.float64) + 0.5) / 2.0 ** 32))
+        codes[sl] = np.where((v > 0) & (k == 0), 1, np.minimum(k, 255))
     return codes, steps
 
 
