@@ -700,7 +700,7 @@ def experts_fwd(x: torch.Tensor, offsets: torch.Tensor, q: QuantizedWeight, A: t
     x: bf16 [M, n], rows in order of their expert; offsets: int32 [E + 1] on the device, expert e's rows being
     offsets[e] .. offsets[e + 1] - 1 (none is fine); q: the experts' weights quantized as one [E m, n] weight; A
     bf16 [E, r, n], B bf16 [E, m, r].  Rows of no expert are not written (where h or u is not given, they hold
-    anything).
+    anything).  M may be 0: a batch that has no row for these experts.
     """
     M, E, n, m, r = _experts(x, offsets, q, A, B)
     if h is None:
@@ -712,6 +712,8 @@ def experts_fwd(x: torch.Tensor, offsets: torch.Tensor, q: QuantizedWeight, A: t
     elif want_u:
         u = torch.empty((M, r), dtype=torch.float32, device=x.device)
     _same_device(x.device, h=h, u=u)
+    if M == 0:
+        return h, u
     with _on(x.device):
         ws = _room(experts_workspace_bytes(QLORA_OP_FWD, M, E, n, m, r), x.device, workspace)
         st = _lib.load().qlora_experts_fwd(M, E, n, m, r, float(s), _ptr(x), _ptr(offsets), _ptr(q.codes),
@@ -743,6 +745,10 @@ def experts_bwd(x: torch.Tensor, g: torch.Tensor, offsets: torch.Tensor, q: Quan
         _need(gA, torch.bfloat16, (E, r, n), "out[1]")
         _need(gB, torch.bfloat16, (E, m, r), "out[2]")
     _same_device(x.device, g=g, u=u, **{"out[0]": gx, "out[1]": gA, "out[2]": gB})
+    if M == 0:  # every expert is one without rows
+        gA.detach().zero_()
+        gB.detach().zero_()
+        return gx, gA, gB
     with _on(x.device):
         ws = _room(experts_workspace_bytes(QLORA_OP_BWD, M, E, n, m, r), x.device, workspace)
         st = _lib.load().qlora_experts_bwd(M, E, n, m, r, float(s), _ptr(x), _ptr(g), _ptr(offsets), _ptr(q.codes),

@@ -574,7 +574,9 @@ qlora_status qlora_preference_bwd(int32_t type, int64_t T, int64_t V, const void
  *   x, h, u_out: as for qlora_linear_fwd, M rows in all; u_out may be NULL.
  * Requires 1 <= E <= 1024, M < 2^22, E m < 2^31, E m n <= 2^40,
  * (M / 256 + E) ceil(max(n, m) / 128) < 2^22, and for each expert the limits
- * of qlora_linear_fwd with all M rows.  No dropout.
+ * of qlora_linear_fwd with all M rows, M >= 1 among them (with no row at all
+ * there is nothing to call: h is empty and the gradients are zero).  No dropout
+ * and no 8-bit checkpoint of x.
  */
 #define QLORA_MAX_EXPERTS 1024
 qlora_status qlora_experts_fwd(int64_t M, int64_t E, int64_t n, int64_t m, int32_t r, float s, const qlora_bf16* x,
