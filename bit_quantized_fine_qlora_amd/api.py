@@ -818,8 +818,8 @@ class AdamWStep:
     tensors: list of (param fp32, param_bf16 bf16 or None, grad bf16 or fp32, exp_avg, exp_avg_sq), the moments
     both fp32 tensors or both Moment8 (signed first); each contiguous with the same number of elements, on one GPU
     or (the gradient too) in pinned host memory.  The tensors' table is written to `device` (a GPU: that of the
-    tensors, or the current one) here, on the current stream; the tensors must stay where they are.  clip() and
-    run() of one AdamWStep must be ordered.
+    tensors, or the current one) here, on the current stream; the tensors must stay where they are, gradients too.
+    clip() and run() of one AdamWStep must be ordered, and on another stream follow this call's.
     """
 
     def __init__(self, tensors, device=None):

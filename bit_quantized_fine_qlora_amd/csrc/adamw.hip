@@ -34,10 +34,11 @@
 // All of it is bound by memory: 16 bytes an element with 8-bit moments (p
 // read and written, the bf16 gradient, the bf16 copy, codes read and
 // written) and 1/8 byte of steps, 28 with 32-bit ones.  Measured: 41.9 million
-// elements in 448 tensors, 8 bits, 116-133 us by card (5.1-5.8 TB/s); 84.9
-// million 231-259 us (5.3-5.9 TB/s); 6.1 million in 97 tensors of odd sizes,
-// 32 bits and fp32 gradients, 30 us (183 MB, 6.1 TB/s, part of it out of the
-// memory-side cache).
+// elements in 448 tensors, 8 bits, 119-143 us by card (4.7-5.7 TB/s); 84.9
+// million 236-264 us (5.2-5.8 TB/s), with drawn codes as long to 16 % longer
+// (alone 151 us against 130, among other steps 156 and 156); 6.1 million in 97
+// tensors of odd sizes, 32 bits and fp32 gradients, 30 us (183 MB, 6.1 TB/s,
+// part of it out of the memory-side cache).
 //
 // The plan.  A step's tensors stay the same over a training run, so their
 // table is written to device memory once: header, room for the norm's partial
@@ -387,9 +388,12 @@ void launch_adamw_step(void* plan, int64_t tensors, int64_t chunks, double lr, d
 // ---------------------------------------------------------------------------
 // The gradients' norm: squares and sums in 64 bits, each workgroup's chunks
 // and then the workgroups' sums in a fixed order.  Bound by the read: 84 MB of
-// bf16 gradients in 448 tensors 21-31 us by card (2.7-4.0 TB/s; four chunks in
-// flight a workgroup, or the table read ahead, were no faster), 2-5 us for the
-// second launch.
+// bf16 gradients in 448 tensors 21-31 us by card (2.7-4.0 TB/s), 2-5 us for the
+// second launch.  A chunk's owner, its tensor's entry and its gradient are read
+// one after the other.  The gradient's address comes out of the table, so its
+// loads are flat ones, which count with the scalar reads too: a look into the
+// table waits for every load in flight, and four chunks at once or the table
+// read ahead were no faster.
 // ---------------------------------------------------------------------------
 
 // Sum over the workgroup's 256 threads, in thread 0.

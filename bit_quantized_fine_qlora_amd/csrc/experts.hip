@@ -67,8 +67,8 @@ __device__ __forceinline__ int wave_scan_add(int v) {
 // are held within 0 .. M and below none before them, so that every row belongs
 // to one expert at most whatever they hold, and the tiles of all experts are as
 // few as the host assumes.  kMany: more than 64 experts (1024 x 4096 x 512,
-// 40000 rows: 1160 us; with a second pass over all offsets, and none on their
-// way, 1340.  One form for all numbers costs 64 x 1024 x 2048 1 us of 55).
+// 40000 rows: 1160 us, its bytes some 290; with a second pass over all offsets,
+// and none on their way, 1340.  One form for all numbers costs 64 x 1024 x 2048 1 us of 55).
 template <bool kMany>
 struct ExpertScan {
   int first = 0;               // expert of lane 0
@@ -247,7 +247,7 @@ static inline int64_t most_tiles(int64_t M, int64_t E, int64_t bt) { return M / 
 // ---------------------------------------------------------------------------
 // 2 rows N K operations against N K / 2 bytes of weights an expert: bound by
 // the matrix units from some 100 rows an expert on.  Measured, r = 16, x 8 of
-// 14336 x 4096 and 8192 rows (962 GFLOP): h 890-1030 us by card, grad_x 940-1050
+// 14336 x 4096 and 8192 rows (962 GFLOP): h 890-1030 us by card, grad_x 890-1050
 // us, 0.92-1.08 PFLOP/s; one dense layer of these sizes takes 770-850 and
 // 730-815 us on the same cards, the difference being the experts' ragged tiles.
 // 64 of 1024 x 2048 and 6000 ragged rows (25 GFLOP, 104 MB): 47 us, of which 14
@@ -519,7 +519,10 @@ __device__ __forceinline__ void lora_rows(const float* part, int splits, int64_t
 // through it, shared by the workgroup's 128 features.  8 x 14336 x 4096 (235 MB
 // of codes, 16 rows): 64-65 us, 3.6 TB/s; the codes' loads alone take 54 us
 // (4.4 TB/s), with x and the barriers 59.  Loads arranged to 64 contiguous
-// bytes a row and swapped between lanes took 69 us, non-temporal loads 67.
+// bytes a row and swapped between lanes took 69 us, non-temporal loads 67.  All
+// workgroups are resident and end together, and lora_rows then adds u's K splits
+// (8 here) one trip to memory after the other, behind B's loads: nothing hides
+// these.
 //
 // Whole calls, us, tiles of 16 rows / tiles of 32 / the GEMM, by rows an expert
 // (r = 16):
@@ -530,6 +533,17 @@ __device__ __forceinline__ void lora_rows(const float* part, int splits, int64_t
 //   64 x 1024 x 2048     25  28  38       38  30  38      52  44  39
 // so tiles of 16 rows up to 16 rows an expert on average, of 32 up to 32, then
 // the GEMM.  Tiles of 64 and 128 rows were no better than it anywhere above.
+// The average is what the host knows.  All rows in k of the experts, forward
+// calls, us, balanced / k of them hold all rows / a call of those k alone:
+//    64 x 1024 x 2048, 2048 rows (32 on average): 32 /  k 2  31 /  40,  k 8  29 /  41
+//    the same, 2560 rows (40, the GEMM):          40 /  k 2  59 /  43,  k 8  57 /  43
+//    8 x 14336 x 4096, 256 rows (32):             78 /  k 1  73 /  60,  k 2  72 /  61
+//    the same, 320 rows (40, the GEMM):          111 /  k 1  97 /  75,  k 2  80 /  72
+//    1024 x 4096 x 512, 32000 rows (31):         747 /  k 8 651 / 164,  k 64 672 / 174
+//    the same, 40000 rows (39, the GEMM):       1158 /  k 8 642 / 209,  k 64 655 / 225
+// so a skew costs little at 64 experts, and up to four times at 1024, on both
+// sides of the rule: streamed, busy experts' weights are read for every 32 rows;
+// in the GEMM, workgroups are launched for the other experts' tiles.
 struct StreamArgs {
   const uint16_t* x;        // M x K
   const uint8_t* codes;

@@ -161,7 +161,9 @@ typedef struct {
  * (the bias corrections are formed in double on the host).  Requires lr,
  * eps >= 0 and weight_decay finite, 0 <= beta1, beta2 < 1.  `tensors` is a
  * host array read before the call returns.  Results match a float64
- * evaluation of the same step to fp32 rounding.
+ * evaluation of the same step to fp32 rounding.  For more tensors than that,
+ * 8-bit moments, fp32 gradients, a clip factor or a decay lr wd below some
+ * 2e-7, where 1 - lr wd in fp32 is a coarse number, qlora_adamw_step.
  */
 qlora_status qlora_adam_step(const qlora_adam_tensor* tensors, int32_t count, float lr, float beta1, float beta2,
                              float eps, float weight_decay, int64_t step, qlora_stream_t stream);
@@ -651,7 +653,9 @@ typedef struct {
  * device memory, written once, after which a step is one launch.  plan_bytes
  * of at least qlora_adamw_plan_bytes (0 on invalid arguments), 16-byte
  * aligned.  `tensors` is a host array read before the call returns.  The plan
- * also holds the sums of qlora_grad_clip: calls on one plan must be ordered.
+ * also holds the sums of qlora_grad_clip: calls on one plan, this one among
+ * them, must be ordered.  It keeps the tensors' addresses, gradients' too: new
+ * ones take a new plan.
  * Writes 32 bytes of host memory at `handle`, which the calls below take.
  */
 typedef struct {
