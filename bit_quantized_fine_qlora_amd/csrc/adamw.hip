@@ -295,7 +295,7 @@ __global__ __launch_bounds__(256) void adamw_step_kernel(void* plan, int64_t ten
     const float big = (float)__builtin_sqrt(vtop);
     const double iv = vtop > 0.0 ? 0x1p126 / vtop : 0.0;
     const float sc = big * c.inv_root_bc2 > 0x1p125f ? 0.25f : 1.0f;
-    const float to_denom = big * c.inv_root_bc2 * sc, eps = __builtin_fmaxf(c.eps * sc, 0x1p-126f);
+    const float to_denom = big * sc * c.inv_root_bc2, eps = __builtin_fmaxf(c.eps * sc, 0x1p-126f);
     const float step_size = c.step_size * sc;
     u32x2 mo = {0u, 0u}, vo = {0u, 0u};
     u32x4 draw[2] = {};

@@ -29,19 +29,23 @@ def gradients(kind, n, rng):
         return g * 2e-35  # roots of 1e-36 .. 1e-35: no step that fp32 holds
     if kind == "small beside large":
         return np.where(np.arange(n) % 128 == 5, g * 1e8, g * 1e-27)
-    return g * 1.6e38     # to 3.2e38: roots past 2^126, fp32 ends at 3.4e38
+    if kind == "large":
+        return g * 1.6e38  # to 3.2e38: roots past 2^126, fp32 ends at 3.4e38
+    # the largest that there are, with zeros between
+    return np.sign(g) * np.where(np.arange(n) % 3 == 0, 0.0, float(np.finfo(np.float32).max))
 
 
-@pytest.mark.parametrize("kind", ["small blocks", "small beside large", "large"])
+@pytest.mark.parametrize("kind", ["small blocks", "small beside large", "large", "largest"])
 def test_updates_at_any_magnitude(Q, kind):
     base.say(f"adamw, {kind}")
     rng = np.random.default_rng(23)
+    hyper = HYPER | dict(beta2=0.9999) if kind == "largest" else HYPER  # whose first root rounds past the largest
     t = base.Tensor(Q, 6, 128 * 5 + 17, (8, torch.float32, True))
     step_of = Q.AdamWStep([t.entry()])
     for step in (1, 2, 3):
         t.g.copy_(torch.from_numpy(gradients(kind, t.n, rng).astype(np.float32)))
-        want = base.expect(t, step, HYPER, 1.0)
+        want = base.expect(t, step, hyper, 1.0)
         assert np.all(np.abs(want[0]) < 100.0)
-        step_of.run(**HYPER, step=step)
+        step_of.run(**hyper, step=step)
         torch.cuda.synchronize()
         base.check_step(t, want, f"{kind} step {step}")
